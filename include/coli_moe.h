@@ -414,6 +414,127 @@ coli_status coli_moe_tier_lookahead(const coli_moe_dims *dims, const coli_moe_we
                                     const coli_moe_tier *next_tier, const uint16_t *x, int T, uint32_t flags,
                                     void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * Balance of the router (the pages name no training; the loss is the usual one
+ * for a top-k softmax router): per-expert counts, mean probabilities and the
+ * balance loss of a routed batch.
+ *   l'     = logits + bias,  p = softmax(l') over all E experts (fp32)
+ *   counts[e] = pairs (t, j) of live tokens with topk_ids[t][j] == e
+ *   n      = live tokens,  f_e = counts[e] / (n k),  P_e = (sum over live t of p[t][e]) / n
+ *   loss   = E * sum_e f_e P_e      (1 for a uniform router; 0 when n == 0)
+ * The counts are what a usage profile of the host-RAM tier holds for a batch.
+ *   logits   fp32 [T][E], bias fp32 [E] or NULL: as for coli_moe_route
+ *   topk_ids int32 [T][k]: as coli_moe_route wrote them.  An id outside [0, E)
+ *            is not counted and sets COLI_FLAG_BAD_ID
+ *   mask     uint8 [T] or NULL: a token with mask 0 (padding) is not live: it is
+ *            neither counted nor averaged, and its row and ids are not looked at
+ *   counts   int32 [E], n_live int32 [1], prob_mean fp32 [E] (P), loss fp32 [1]: out
+ *   ws       device scratch of at least coli_moe_balance_workspace_bytes(T, E)
+ *            bytes, 256-byte aligned; contents on entry are ignored
+ * A NaN logit counts as -inf and a +inf one takes the row's whole mass (shared
+ * evenly among several); both set COLI_FLAG_NONFINITE.  A row with nothing above
+ * -inf has p = 0.  1 <= k <= min(E, 32), E <= 1024, T*k <= 2^24, T == 0 gives
+ * zeros.  Sums are taken in a fixed order: the same inputs give the same bits.
+ */
+coli_status coli_moe_balance(const float *logits, const float *bias, const int32_t *topk_ids, const uint8_t *mask,
+                             int T, int E, int k, int32_t *counts, int32_t *n_live, float *prob_mean, float *loss,
+                             void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of the router's logits: of grad_loss * loss (coli_moe_balance), and of
+ * the renormalised weights of coli_moe_route, in one pass.
+ *   d_logits[t][e] = grad_loss * E/n * p[t][e] * (f_e - sum_i p[t][i] f_i)
+ *                  + sum over j with topk_ids[t][j] == e of w_j (dw_j - sum_i w_i dw_i)
+ * for live tokens, 0 for the others.  f is piecewise constant: no gradient.
+ *   logits, bias, mask, counts, n_live: as given to / written by coli_moe_balance
+ *   grad_loss  fp32 [1] (device) or NULL: no loss term
+ *   topk_ids, topk_w, d_topk_w  [T][k]: the routing and the gradient of its
+ *              weights; d_topk_w NULL: no weight term (the other two may be NULL
+ *              then).  Ids outside [0, E) get nothing.  One of grad_loss and
+ *              d_topk_w is required
+ *   d_logits   fp32 [T][E] out (written, not added to; may be logits itself)
+ *   d_bias     fp32 [E] out or NULL: the sum of d_logits over the tokens
+ *   ws         as for coli_moe_balance (its contents are ignored, so the two
+ *              calls may share it on one stream)
+ */
+coli_status coli_moe_balance_backward(const float *logits, const float *bias, const uint8_t *mask,
+                                      const int32_t *counts, const int32_t *n_live, const float *grad_loss,
+                                      const int32_t *topk_ids, const float *topk_w, const float *d_topk_w, int T,
+                                      int E, int k, float *d_logits, float *d_bias, void *ws, size_t ws_bytes,
+                                      void *stream);
+
+/* Workspace bytes of the two calls above for up to T_max tokens; 0 for invalid
+ * arguments.  Host only. */
+size_t coli_moe_balance_workspace_bytes(int T_max, int E);
+
+/*
+ * Residual addition, root-mean-square norm and 8-bit rows (the layer's pre-norm
+ * with a residual and a weight, for the 8-bit products below):
+ *   s = bf16(x + residual)                          (s = x without a residual)
+ *   n = s / sqrt(mean(s^2) + eps) * weight          (fp32; weight 1 when NULL)
+ *   per 128 columns: c = max(max|n| / 448, 2^-126),  q = e4m3(n / c)
+ *   x, residual  bf16 [T][H]; residual NULL: none
+ *   weight   bf16 [H] or NULL
+ *   sum_out  bf16 [T][H] or NULL: s; may be x or residual (in place)
+ *   norm_out bf16 [T][H] or NULL: bf16(n), e.g. the router's input
+ *   q        e4m3 [T][H] (bytes), q_scale fp32 [T][H/128]: n ~ q * q_scale
+ * H a multiple of 128, H <= 32768; bf16 tensors and q 16-byte aligned; eps >= 0.
+ * A row whose sum of squares is not finite sets COLI_FLAG_NONFINITE; its
+ * outputs are what the formulas give (NaN codes are 0x7f).
+ */
+coli_status coli_add_rmsnorm_fp8(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps, int T,
+                                 int H, uint16_t *sum_out, uint16_t *norm_out, uint8_t *q, float *q_scale,
+                                 void *stream);
+
+/*
+ * Matrix product of 8-bit floating-point codes (e4m3) with a scale for each
+ * block of 128:
+ *   out[m][n] = sum_b a_scale[m][b] * w_scale[n/128][b] * sum_{k in block b} a[m][k] * w[n][k]
+ *   a  e4m3 [M][K], a_scale fp32 [M][ceil(K/128)]: as coli_add_rmsnorm_fp8 writes them
+ *   w  e4m3 [N][K], w_scale fp32 [ceil(N/128)][ceil(K/128)]
+ *   out  bf16 [M][N], or fp32 with COLI_FP8_OUT_F32
+ * K a multiple of 16 (the last block may be short), K <= 2^20; any N <= 2^21, M
+ * <= 2^24; M == 0 is a no-op.  a, w and out 16-byte aligned; out overlaps no
+ * input.  A block's products are summed in fp32 on the tensor cores; the scaled
+ * block sums are added in fp32 in a fixed order.
+ */
+#define COLI_FP8_OUT_F32 0x1u
+coli_status coli_fp8_matmul(const uint8_t *a, const float *a_scale, const uint8_t *w, const float *w_scale, int M,
+                            int N, int K, void *out, uint32_t flags, void *stream);
+
+/*
+ * Expert FFN + combine over 8-bit floating-point experts (the form the
+ * converter's source checkpoints have; the counterpart of coli_moe_expert_ffn,
+ * for a batch routed by coli_moe_route and coli_moe_union):
+ *   g = W_gate x, u = W_up x (products as in coli_fp8_matmul, kept in fp32)
+ *   h = silu(g) * u, as e4m3 codes with one scale per token and 128 columns
+ *       (c = max(max|h| / 448, 2^-126), rounded from the fp32 h)
+ *   y = W_down h (fp32);  out[t] = bf16( sum_j w[t,j] y_{id[t,j]} + sum_s y_{E+s} + residual[t] )
+ * Weights (row-major, K contiguous, experts then shared experts):
+ *   gate_q, up_q e4m3 [E+S][I][H]   gate_s, up_s fp32 [E+S][I/128][H/128]
+ *   down_q       e4m3 [E+S][H][I]   down_s       fp32 [E+S][H/128][I/128]
+ * dims: group == 128, code_bits == 8; H and I multiples of 128; E <= 1024, 1 <=
+ * k <= min(E, 32), S <= 4, T*(k+S) <= 2^24.
+ *   x        e4m3 [T][H], x_scale fp32 [T][H/128] (coli_add_rmsnorm_fp8)
+ *   the routing arrays, residual and out: as for coli_moe_expert_ffn (out may
+ *   alias residual)
+ *   ws       at least coli_moe_fp8_workspace_bytes(dims, T), 256-byte aligned
+ */
+typedef struct {
+  const uint8_t *gate_q, *up_q, *down_q;
+  const float *gate_s, *up_s, *down_s;
+} coli_moe_weights_fp8;
+
+coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims *dims, const coli_moe_weights_fp8 *w, const uint8_t *x,
+                                    const float *x_scale, int T, const int32_t *topk_ids, const float *topk_w,
+                                    const int32_t *unique_ids, const int32_t *n_unique, const int32_t *seg_off,
+                                    const int32_t *perm, const int32_t *pair_pos, const uint16_t *residual,
+                                    uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes of coli_moe_expert_ffn_fp8 for up to T_max tokens; 0 for
+ * unsupported dims.  Host only. */
+size_t coli_moe_fp8_workspace_bytes(const coli_moe_dims *dims, int T_max);
+
 /* Static description of a status code. */
 const char *coli_status_str(coli_status s);
 

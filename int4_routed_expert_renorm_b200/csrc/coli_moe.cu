@@ -14,9 +14,12 @@
 #include <utility>
 
 #include "common.cuh"
+#include "k_balance.cuh"
 #include "k_ffn_decode.cuh"
 #include "k_ffn_prefill.cuh"
 #include "k_ffn_splitk.cuh"
+#include "k_fp8_gemm.cuh"
+#include "k_norm_fp8.cuh"
 #include "k_router.cuh"
 #include "k_tier.cuh"
 #include "k_union.cuh"
@@ -1384,3 +1387,5 @@ coli_status coli_moe_get_status(void* stream, uint32_t* flags) {
 }
 
 }  // extern "C"
+
+#include "ops_api.cuh"

@@ -1,0 +1,137 @@
+// Residual addition, root-mean-square norm and 8-bit rows with block scales.
+//
+//   s = bf16(x + r)                      (s = x without a residual)
+//   n = s * (mean(s^2) + eps)^(-1/2) * g (g = 1 without a weight), in fp32
+//   per 128 columns: c = max(max|n| / 448, 2^-126),  q = e4m3(n / c)
+// 448 is e4m3's largest value, so the block's largest |n| lands on it.  The
+// codes are rounded from the fp32 n, not from its bf16 copy.  The floor 2^-126
+// keeps the scale a normal number for blocks of zeros.
+//
+// One block of 256 threads per row; a thread holds 8 consecutive values per 2048
+// columns (one 16-byte load), so a 128-column block is 16 neighbouring lanes and
+// its maximum a 4-step shuffle.  The row is read once and stays in registers.
+// Bound by HBM for large batches (9.03 bytes per value with everything written)
+// and by latency for single tokens.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace coli {
+
+constexpr int kF8Block = 128;           // columns (and weight rows) per scale
+constexpr float kF8Max = 448.0f;        // largest e4m3 value
+constexpr float kF8MinScale = 1.17549435e-38f;   // 2^-126
+
+// max(a, b) that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The scale of a block whose largest magnitude is m, and its inverse.
+__device__ __forceinline__ float f8_scale(float m, float* inv) {
+  const float c = max_nan(m / kF8Max, kF8MinScale);
+  *inv = 1.0f / c;
+  return c;
+}
+
+// Four values as e4m3 bytes (round to nearest even, saturating, NaN kept).
+__device__ __forceinline__ uint32_t f8x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  return float_to_bf16_bits(a) | (static_cast<uint32_t>(float_to_bf16_bits(b)) << 16);
+}
+
+// NC: 2048-column steps of a row (H <= 2048 * NC).  x, residual and sum_out may
+// be the same buffer: a thread reads its values before it writes them.
+template <int NC>
+__global__ void __launch_bounds__(256)
+    add_rmsnorm_fp8_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,
+                           int H, uint16_t* sum_out, uint16_t* __restrict__ norm_out, uint8_t* __restrict__ q,
+                           float* __restrict__ q_scale, uint32_t* __restrict__ status) {
+  __shared__ float sm[8];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const size_t row = static_cast<size_t>(blockIdx.x) * H;
+  uint4 v[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (i * 256 + tid) * 8;
+    v[i] = c < H ? *reinterpret_cast<const uint4*>(x + row + c) : make_uint4(0, 0, 0, 0);
+  }
+  if (residual) {
+    uint4 r[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int c = (i * 256 + tid) * 8;
+      r[i] = c < H ? *reinterpret_cast<const uint4*>(residual + row + c) : make_uint4(0, 0, 0, 0);
+    }
+    auto add2 = [](uint32_t a, uint32_t b) {
+      return bf16x2(__uint_as_float(a << 16) + __uint_as_float(b << 16),
+                    __uint_as_float(a & 0xffff0000u) + __uint_as_float(b & 0xffff0000u));
+    };
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      v[i] = make_uint4(add2(v[i].x, r[i].x), add2(v[i].y, r[i].y), add2(v[i].z, r[i].z), add2(v[i].w, r[i].w));
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (i * 256 + tid) * 8;
+    if (sum_out && c < H) *reinterpret_cast<uint4*>(sum_out + row + c) = v[i];
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xffff0000u);
+      ss = fmaf(a, a, ss);
+      ss = fmaf(b, b, ss);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (lane == 0) sm[warp] = ss;
+  __syncthreads();
+  ss = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
+  if (tid == 0 && !(ss < INFINITY)) atomicOr(status, COLI_FLAG_NONFINITE);
+  const float rs = 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
+  const int nb = H / kF8Block;
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int c = (i * 256 + tid) * 8;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint4 gw = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);   // bf16 ones
+    if (weight && c < H) gw = __ldg(reinterpret_cast<const uint4*>(weight + c));
+    const uint32_t g[4] = {gw.x, gw.y, gw.z, gw.w};
+    float n[8];
+    float m = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      n[2 * k] = __uint_as_float(w[k] << 16) * rs * __uint_as_float(g[k] << 16);
+      n[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * rs * __uint_as_float(g[k] & 0xffff0000u);
+      m = max_nan(m, max_nan(fabsf(n[2 * k]), fabsf(n[2 * k + 1])));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (c < H) {
+      float inv;
+      const float sc = f8_scale(m, &inv);
+      if ((lane & 15) == 0) q_scale[static_cast<size_t>(blockIdx.x) * nb + c / kF8Block] = sc;
+      uint2 o;
+      o.x = f8x4(n[0] * inv, n[1] * inv, n[2] * inv, n[3] * inv);
+      o.y = f8x4(n[4] * inv, n[5] * inv, n[6] * inv, n[7] * inv);
+      *reinterpret_cast<uint2*>(q + row + c) = o;
+      if (norm_out)
+        *reinterpret_cast<uint4*>(norm_out + row + c) =
+            make_uint4(bf16x2(n[0], n[1]), bf16x2(n[2], n[3]), bf16x2(n[4], n[5]), bf16x2(n[6], n[7]));
+    }
+  }
+}
+
+}  // namespace coli

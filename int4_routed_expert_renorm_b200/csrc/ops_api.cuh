@@ -1,0 +1,300 @@
+// Host side of the balance loss and the 8-bit floating-point operators.
+// Part of coli_moe.cu (included there, after the launch helpers).
+#pragma once
+
+namespace {
+
+// ---- balance ---------------------------------------------------------------
+
+// Blocks of a balance pass: a token per warp, at most two blocks per SM of the
+// largest part (148 SMs), so that the workspace depends on T and E alone.
+inline int balance_blocks(int T) { return std::min((T + kBalWarps - 1) / kBalWarps, 296); }
+
+struct BalWs {
+  float* p;      // [blocks][E] column sums
+  int32_t* c;    // [blocks][E] pair counts
+  int32_t* n;    // [blocks] live tokens
+  size_t bytes;
+};
+
+BalWs balance_layout(int T, int E, void* base) {
+  BalWs w{};
+  const size_t nb = static_cast<size_t>(balance_blocks(T));
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t o = 0;
+  auto take = [&](size_t bytes) -> void* {
+    void* p = b ? b + o : nullptr;
+    o += align256(bytes);
+    return p;
+  };
+  w.p = static_cast<float*>(take(nb * E * 4));
+  w.c = static_cast<int32_t*>(take(nb * E * 4));
+  w.n = static_cast<int32_t*>(take(nb * 4));
+  w.bytes = o;
+  return w;
+}
+
+coli_status check_balance(int T, int E, int k) {
+  if (T < 0 || E < 1 || k < 1) return COLI_ERR_INVALID_ARG;
+  if (E > 1024 || k > 32 || k > E || static_cast<int64_t>(T) * k > (int64_t(1) << 24)) return COLI_ERR_UNSUPPORTED;
+  return COLI_OK;
+}
+
+// Rows move as 16-byte loads when every row starts on a 16-byte boundary.
+inline bool balance_vec4(int E, const void* a, const void* b, const void* c) {
+  return E % 4 == 0 && aligned(a, 16) && aligned(b, 16) && aligned(c, 16);
+}
+
+#define COLI_BAL_DISPATCH(E, vec, CALL)                                        \
+  switch (route_nv(E)) {                                                       \
+    case 1: case 2: case 4:                                                    \
+      ok = vec ? CALL(4, 4) : CALL(4, 1); break;                               \
+    case 8: ok = vec ? CALL(8, 4) : CALL(8, 1); break;                         \
+    case 16: ok = vec ? CALL(16, 4) : CALL(16, 1); break;                      \
+    default: ok = vec ? CALL(32, 4) : CALL(32, 1); break;                      \
+  }
+
+// ---- 8-bit floating point ----------------------------------------------------
+
+coli_status check_dims_fp8(const coli_moe_dims* d) {
+  if (!d) return COLI_ERR_INVALID_ARG;
+  if (d->group != kF8Block || d->code_bits != 8) return COLI_ERR_UNSUPPORTED;
+  if (d->hidden <= 0 || d->hidden % kF8Block != 0 || d->inter <= 0 || d->inter % kF8Block != 0)
+    return COLI_ERR_UNSUPPORTED;
+  if (d->n_experts < 1 || d->n_experts > 1024) return COLI_ERR_UNSUPPORTED;
+  if (d->top_k < 1 || d->top_k > 32 || d->top_k > d->n_experts) return COLI_ERR_UNSUPPORTED;
+  if (d->n_shared < 0 || d->n_shared > 4) return COLI_ERR_UNSUPPORTED;
+  const int64_t n = d->n_experts + d->n_shared, r = std::max(d->hidden, d->inter);
+  if (n * r > INT32_MAX / 2) return COLI_ERR_UNSUPPORTED;
+  return COLI_OK;
+}
+
+struct F8Ws {
+  uint8_t* hq;    // [P+S*T][I] codes of h
+  float* hs;      // [P+S*T][I/128]
+  float* gate;    // [P+S*T][I]
+  float* up;
+  float* y;       // [P+S*T][H]
+  size_t bytes;
+};
+
+F8Ws fp8_layout(const coli_moe_dims* d, int T, void* base) {
+  F8Ws w{};
+  const size_t rows = static_cast<size_t>(T) * (d->top_k + d->n_shared), I = d->inter, H = d->hidden;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  size_t o = 0;
+  auto take = [&](size_t bytes) -> void* {
+    void* p = b ? b + o : nullptr;
+    o += align256(bytes);
+    return p;
+  };
+  w.hq = static_cast<uint8_t*>(take(rows * I));
+  w.hs = static_cast<float*>(take(rows * (I / kF8Block) * 4));
+  w.gate = static_cast<float*>(take(rows * I * 4));
+  w.up = static_cast<float*>(take(rows * I * 4));
+  w.y = static_cast<float*>(take(rows * H * 4));
+  w.bytes = o;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t coli_moe_balance_workspace_bytes(int T_max, int E) {
+  if (T_max < 0 || E < 1 || E > 1024) return 0;
+  return balance_layout(std::max(T_max, 1), E, nullptr).bytes;
+}
+
+coli_status coli_moe_balance(const float* logits, const float* bias, const int32_t* topk_ids, const uint8_t* mask,
+                             int T, int E, int k, int32_t* counts, int32_t* n_live, float* prob_mean, float* loss,
+                             void* ws, size_t ws_bytes, void* stream) {
+  const coli_status st = check_balance(T, E, k);
+  if (st != COLI_OK) return st;
+  if ((T > 0 && (!logits || !topk_ids)) || !counts || !n_live || !prob_mean || !loss || !ws || !aligned(ws, 256))
+    return COLI_ERR_INVALID_ARG;
+  const BalWs w = balance_layout(std::max(T, 1), E, ws);
+  if (ws_bytes < w.bytes) return COLI_ERR_WORKSPACE;
+  DevInfo di;
+  if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
+  const cudaStream_t s = as_stream(stream);
+  const int blocks = balance_blocks(T);   // 0 for an empty batch: counts, means and loss are zero
+  if (T > 0) {
+    const bool vec = balance_vec4(E, logits, bias, nullptr);
+    const size_t smem = static_cast<size_t>(kBalWarps + 1) * E * 4;
+    bool ok;
+#define COLI_BAL_FWD(NV, VEC)                                                                                     \
+  launch(balance_partial_kernel<NV, VEC>, dim3(blocks), dim3(kBalWarps * 32), smem, s, logits, bias, topk_ids, mask, \
+         T, E, k, w.p, w.c, w.n, di.status)
+    COLI_BAL_DISPATCH(E, vec, COLI_BAL_FWD)
+#undef COLI_BAL_FWD
+    if (!ok) return COLI_ERR_CUDA;
+  }
+  return launch(balance_finish_kernel, dim3(1), dim3(1024), 0, s, static_cast<const float*>(w.p),
+                static_cast<const int32_t*>(w.c), static_cast<const int32_t*>(w.n), blocks, E, k, counts, n_live,
+                prob_mean, loss)
+             ? COLI_OK
+             : COLI_ERR_CUDA;
+}
+
+coli_status coli_moe_balance_backward(const float* logits, const float* bias, const uint8_t* mask,
+                                      const int32_t* counts, const int32_t* n_live, const float* grad_loss,
+                                      const int32_t* topk_ids, const float* topk_w, const float* d_topk_w, int T,
+                                      int E, int k, float* d_logits, float* d_bias, void* ws, size_t ws_bytes,
+                                      void* stream) {
+  const coli_status st = check_balance(T, E, k);
+  if (st != COLI_OK) return st;
+  if (!counts || !n_live || (!grad_loss && !d_topk_w) || !ws || !aligned(ws, 256)) return COLI_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !d_logits || (d_topk_w && (!topk_ids || !topk_w)))) return COLI_ERR_INVALID_ARG;
+  const BalWs w = balance_layout(std::max(T, 1), E, ws);
+  if (ws_bytes < w.bytes) return COLI_ERR_WORKSPACE;
+  DevInfo di;
+  if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
+  const cudaStream_t s = as_stream(stream);
+  const int blocks = balance_blocks(T);
+  if (T > 0) {
+    const bool vec = balance_vec4(E, logits, bias, d_logits);
+    const size_t smem = d_bias ? static_cast<size_t>(kBalWarps) * E * 4 : 0;
+    float* part = d_bias ? w.p : nullptr;
+    bool ok;
+#define COLI_BAL_BWD(NV, VEC)                                                                                  \
+  launch(balance_backward_kernel<NV, VEC>, dim3(blocks), dim3(kBalWarps * 32), smem, s, logits, bias, mask, counts, \
+         n_live, grad_loss, topk_ids, topk_w, d_topk_w, T, E, k, d_logits, part)
+    COLI_BAL_DISPATCH(E, vec, COLI_BAL_BWD)
+#undef COLI_BAL_BWD
+    if (!ok) return COLI_ERR_CUDA;
+  }
+  if (d_bias && !launch(balance_bias_kernel, dim3((E + 255) / 256), dim3(256), 0, s, static_cast<const float*>(w.p),
+                        blocks, E, d_bias))
+    return COLI_ERR_CUDA;
+  return COLI_OK;
+}
+
+coli_status coli_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, float eps, int T,
+                                 int H, uint16_t* sum_out, uint16_t* norm_out, uint8_t* q, float* q_scale,
+                                 void* stream) {
+  if (T < 0 || H < 1 || !(eps >= 0.f)) return COLI_ERR_INVALID_ARG;
+  if (H % kF8Block != 0 || H > 32768 || T > (1 << 24)) return COLI_ERR_UNSUPPORTED;
+  if (T == 0) return COLI_OK;
+  if (!x || !q || !q_scale) return COLI_ERR_INVALID_ARG;
+  const void* ps[6] = {x, residual, weight, sum_out, norm_out, q};
+  for (const void* p : ps)
+    if (!aligned(p, 16)) return COLI_ERR_INVALID_ARG;
+  if (!aligned(q_scale, 4) || norm_out == x || (residual && norm_out == residual) || (norm_out && norm_out == sum_out))
+    return COLI_ERR_INVALID_ARG;
+  DevInfo di;
+  if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
+  const cudaStream_t s = as_stream(stream);
+  const int nc = (H + 2047) / 2048;
+  bool ok;
+#define COLI_NORM(NC)                                                                                             \
+  launch(add_rmsnorm_fp8_kernel<NC>, dim3(T), dim3(256), 0, s, x, residual, weight, eps, H, sum_out, norm_out, q, \
+         q_scale, di.status)
+  if (nc <= 1) ok = COLI_NORM(1);
+  else if (nc <= 2) ok = COLI_NORM(2);
+  else if (nc <= 3) ok = COLI_NORM(3);
+  else if (nc <= 4) ok = COLI_NORM(4);
+  else if (nc <= 8) ok = COLI_NORM(8);
+  else ok = COLI_NORM(16);
+#undef COLI_NORM
+  return ok ? COLI_OK : COLI_ERR_CUDA;
+}
+
+coli_status coli_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_t* w, const float* w_scale, int M,
+                            int N, int K, void* out, uint32_t flags, void* stream) {
+  if (M < 0 || N < 1 || K < 1 || (flags & ~COLI_FP8_OUT_F32)) return COLI_ERR_INVALID_ARG;
+  if (K % 16 != 0 || K > (1 << 20) || N > (1 << 21) || M > (1 << 24)) return COLI_ERR_UNSUPPORTED;
+  if (M == 0) return COLI_OK;
+  if (!a || !a_scale || !w || !w_scale || !out) return COLI_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4))
+    return COLI_ERR_INVALID_ARG;
+  DevInfo di;
+  if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
+  F8Gemm g{};
+  g.a = a;
+  g.a_s = a_scale;
+  g.w = w;
+  g.w_s = w_scale;
+  g.out = out;
+  g.M = M;
+  g.R = N;
+  g.K = K;
+  g.out_f32 = (flags & COLI_FP8_OUT_F32) ? 1 : 0;
+  return launch(fp8_gemm_simple_kernel, dim3((M + 63) / 64, (N + 63) / 64), dim3(256), 0, as_stream(stream), g)
+             ? COLI_OK
+             : COLI_ERR_CUDA;
+}
+
+size_t coli_moe_fp8_workspace_bytes(const coli_moe_dims* dims, int T_max) {
+  if (check_dims_fp8(dims) != COLI_OK || T_max < 0) return 0;
+  return fp8_layout(dims, std::max(T_max, 1), nullptr).bytes;
+}
+
+coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims* dims, const coli_moe_weights_fp8* w, const uint8_t* x,
+                                    const float* x_scale, int T, const int32_t* topk_ids, const float* topk_w,
+                                    const int32_t* unique_ids, const int32_t* n_unique, const int32_t* seg_off,
+                                    const int32_t* perm, const int32_t* pair_pos, const uint16_t* residual,
+                                    uint16_t* out, void* ws, size_t ws_bytes, void* stream) {
+  const coli_status st = check_dims_fp8(dims);
+  if (st != COLI_OK) return st;
+  if (T < 0) return COLI_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(T) * (dims->top_k + dims->n_shared) > (int64_t(1) << 24)) return COLI_ERR_UNSUPPORTED;
+  if (!w || !w->gate_q || !w->up_q || !w->down_q || !w->gate_s || !w->up_s || !w->down_s) return COLI_ERR_INVALID_ARG;
+  if (T == 0) return COLI_OK;
+  if (!x || !x_scale || !topk_ids || !topk_w || !unique_ids || !n_unique || !seg_off || !perm || !pair_pos || !out || !ws)
+    return COLI_ERR_INVALID_ARG;
+  const void* ps[9] = {w->gate_q, w->up_q, w->down_q, w->gate_s, w->up_s, w->down_s, x, out, residual};
+  for (const void* p : ps)
+    if (!aligned(p, 16)) return COLI_ERR_INVALID_ARG;
+  if (!aligned(x_scale, 4) || !aligned(ws, 256)) return COLI_ERR_INVALID_ARG;
+  const F8Ws lay = fp8_layout(dims, T, ws);
+  if (ws_bytes < lay.bytes) return COLI_ERR_WORKSPACE;
+  DevInfo di;
+  if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
+  const cudaStream_t s = as_stream(stream);
+  const int H = dims->hidden, I = dims->inter, E = dims->n_experts, k = dims->top_k, S = dims->n_shared, P = T * k;
+  F8Gemm g{};
+  g.unique_ids = unique_ids;
+  g.n_unique = n_unique;
+  g.seg_off = seg_off;
+  g.perm = perm;
+  g.T = T;
+  g.k = k;
+  g.E = E;
+  g.S = S;
+  g.P = P;
+  g.out_f32 = 1;
+  g.a = x;
+  g.a_s = x_scale;
+  g.R = I;
+  g.K = H;
+  g.gather = 1;
+  const int blocks = std::min(P, E) + P / 64 + S * ((T + 63) / 64);
+  for (int m = 0; m < 2; ++m) {
+    g.w = m ? w->up_q : w->gate_q;
+    g.w_s = m ? w->up_s : w->gate_s;
+    g.out = m ? lay.up : lay.gate;
+    if (!launch(fp8_gemm_simple_kernel, dim3(blocks, (I + 63) / 64), dim3(256), 0, s, g)) return COLI_ERR_CUDA;
+  }
+  const long hb = static_cast<long>(P + S * T) * (I / kF8Block);
+  if (!launch(swiglu_fp8_kernel, dim3(static_cast<unsigned>(std::min<long>((hb + 7) / 8, 8L * di.sms))), dim3(256), 0,
+              s, static_cast<const float*>(lay.gate), static_cast<const float*>(lay.up), hb, lay.hq, lay.hs))
+    return COLI_ERR_CUDA;
+  g.a = lay.hq;
+  g.a_s = lay.hs;
+  g.w = w->down_q;
+  g.w_s = w->down_s;
+  g.out = lay.y;
+  g.R = H;
+  g.K = I;
+  g.gather = 0;
+  if (!launch(fp8_gemm_simple_kernel, dim3(blocks, (H + 63) / 64), dim3(256), 0, s, g)) return COLI_ERR_CUDA;
+  const long work = static_cast<long>(T) * (H / 4);
+  return launch(combine_kernel, dim3(static_cast<unsigned>(std::min<long>((work + 255) / 256, 16L * di.sms))), dim3(256),
+                0, s, static_cast<const float*>(lay.y), pair_pos, topk_w, residual, T, k, S, H, out,
+                static_cast<const int32_t*>(nullptr), 0, E, static_cast<float*>(nullptr))
+             ? COLI_OK
+             : COLI_ERR_CUDA;
+}
+
+}  // extern "C"
