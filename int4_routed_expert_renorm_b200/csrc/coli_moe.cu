@@ -93,6 +93,24 @@ int g_num_sms[kMaxDevices] = {};
 bool g_attr_done[kMaxDevices] = {};
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
+// Shared memory of the 8-bit product's kernels.  Their setmaxnreg split hands out
+// the registers of a launch at 168 a thread: a build with fewer must not run.
+template <int NMAT, int NT, bool GU>
+bool fp8_kernel_ready() {
+  cudaFuncAttributes at;
+  return cudaFuncSetAttribute(fp8_gemm_kernel<NMAT, NT, GU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(F8Cfg<NMAT, NT>::SMEM)) == cudaSuccess &&
+         cudaFuncGetAttributes(&at, fp8_gemm_kernel<NMAT, NT, GU>) == cudaSuccess && at.numRegs >= 168;
+}
+
+constexpr int kF8Tokens = 160;   // tokens of a tile of the 8-bit product when there are more than 32
+
+bool fp8_kernels_ready() {
+  return fp8_kernel_ready<2, 32, true>() && fp8_kernel_ready<2, kF8Tokens, true>() && fp8_kernel_ready<2, 32, false>() &&
+         fp8_kernel_ready<2, kF8Tokens, false>() && fp8_kernel_ready<1, 32, false>() &&
+         fp8_kernel_ready<1, kF8Tokens, false>();
+}
+
 struct DevInfo {
   uint32_t* status;
   int sms;
@@ -146,6 +164,7 @@ coli_status dev_info(DevInfo* out) {
     COLI_SET_SK_SMEM(1, 64, 8)
     COLI_SET_SK_SMEM(2, 64, 8)
 #undef COLI_SET_SK_SMEM
+    ok &= fp8_kernels_ready();
     ok &= cudaFuncSetAttribute(logits_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
           cudaSuccess;
     ok &= cudaFuncSetAttribute(union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -72,8 +72,6 @@ coli_status check_dims_fp8(const coli_moe_dims* d) {
 struct F8Ws {
   uint8_t* hq;    // [P+S*T][I] codes of h
   float* hs;      // [P+S*T][I/128]
-  float* gate;    // [P+S*T][I]
-  float* up;
   float* y;       // [P+S*T][H]
   size_t bytes;
 };
@@ -90,11 +88,46 @@ F8Ws fp8_layout(const coli_moe_dims* d, int T, void* base) {
   };
   w.hq = static_cast<uint8_t*>(take(rows * I));
   w.hs = static_cast<float*>(take(rows * (I / kF8Block) * 4));
-  w.gate = static_cast<float*>(take(rows * I * 4));
-  w.up = static_cast<float*>(take(rows * I * 4));
   w.y = static_cast<float*>(take(rows * H * 4));
   w.bytes = o;
   return w;
+}
+
+// Tensor maps of one launch: weights (two matrices of the same shape, or one),
+// token rows in boxes of 128, 64, 32 and 16 rows, and single rows to gather.
+bool fp8_maps(CUtensorMap* m, const uint8_t* w0, const uint8_t* w1, int64_t w_rows, const uint8_t* a, int64_t a_rows,
+              int K) {
+  auto enc = [&](CUtensorMap* out, const uint8_t* p, int64_t rows, uint32_t box) {
+    return encode_2d(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, K, rows, K, kF8Block, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  bool ok = enc(&m[0], w0, w_rows, 128) && enc(&m[1], w1 ? w1 : w0, w_rows, 128);
+  for (int j = 0; ok && j < 4; ++j) ok = enc(&m[2 + j], a, a_rows, 128u >> j);
+  return ok && enc(&m[6], a, a_rows, 1);
+}
+
+// One product over `tiles` tiles (an upper bound for routed batches): persistent
+// CTAs, or `split` of them in a cluster for each tile.
+template <int NMAT, int NT, bool GU>
+bool launch_fp8(const CUtensorMap* m, const F8Args& a, int64_t tiles, int split, int sms, cudaStream_t st) {
+  auto kernel = fp8_gemm_kernel<NMAT, NT, GU>;
+  using C = F8Cfg<NMAT, NT>;
+  if (tiles < 1) return true;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(split > 1 ? tiles * split : std::min<int64_t>(tiles, sms)));
+  cfg.blockDim = dim3(kF8Threads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  ++t_launches;
+  return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], m[4], m[5], m[6], a, split) == cudaSuccess;
 }
 
 }  // namespace
@@ -210,19 +243,34 @@ coli_status coli_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
     return COLI_ERR_INVALID_ARG;
   DevInfo di;
   if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
-  F8Gemm g{};
-  g.a = a;
+  const int nk = (K + kF8Block - 1) / kF8Block, nrb = (N + kF8Block - 1) / kF8Block;
+  F8Args g{};
   g.a_s = a_scale;
-  g.w = w;
   g.w_s = w_scale;
   g.out = out;
+  g.status = di.status;
   g.M = M;
   g.R = N;
-  g.K = K;
+  g.nk = nk;
   g.out_f32 = (flags & COLI_FP8_OUT_F32) ? 1 : 0;
-  return launch(fp8_gemm_simple_kernel, dim3((M + 63) / 64, (N + 63) / 64), dim3(256), 0, as_stream(stream), g)
-             ? COLI_OK
-             : COLI_ERR_CUDA;
+  CUtensorMap maps[7];
+  if (!fp8_maps(maps, w, nullptr, N, a, M, K)) return COLI_ERR_CUDA;
+  const cudaStream_t s = as_stream(stream);
+  const bool few = M <= 32;
+  const int64_t blocks = few ? 1 : (M + kF8Tokens - 1) / kF8Tokens;
+  const int64_t tiles1 = blocks * nrb, tiles2 = blocks * ((nrb + 1) / 2);
+  bool ok;
+  if (tiles2 >= di.sms) {
+    ok = few ? launch_fp8<2, 32, false>(maps, g, tiles2, 1, di.sms, s)
+             : launch_fp8<2, kF8Tokens, false>(maps, g, tiles2, 1, di.sms, s);
+  } else {
+    // fewer tiles than SMs: single weight blocks, and several CTAs per tile
+    int split = static_cast<int>(std::min<int64_t>({kF8MaxSplit, di.sms / tiles1, nk / 2}));
+    if (split < 1) split = 1;
+    ok = few ? launch_fp8<1, 32, false>(maps, g, tiles1, split, di.sms, s)
+             : launch_fp8<1, kF8Tokens, false>(maps, g, tiles1, split, di.sms, s);
+  }
+  return ok ? COLI_OK : COLI_ERR_CUDA;
 }
 
 size_t coli_moe_fp8_workspace_bytes(const coli_moe_dims* dims, int T_max) {
@@ -253,42 +301,50 @@ coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims* dims, const coli_moe_we
   if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
   const int H = dims->hidden, I = dims->inter, E = dims->n_experts, k = dims->top_k, S = dims->n_shared, P = T * k;
-  F8Gemm g{};
+  F8Args g{};
+  g.status = di.status;
   g.unique_ids = unique_ids;
   g.n_unique = n_unique;
   g.seg_off = seg_off;
-  g.perm = perm;
   g.T = T;
   g.k = k;
   g.E = E;
   g.S = S;
   g.P = P;
-  g.out_f32 = 1;
-  g.a = x;
+  const bool few = T <= 32;
+  const int nt = few ? 32 : kF8Tokens;
+  const int64_t blocks_ub = static_cast<int64_t>(std::min(P, E)) + P / nt + static_cast<int64_t>(S) * (T / nt + 1);
+  const int64_t rows = static_cast<int64_t>(P) + static_cast<int64_t>(S) * T;
+  // gate and up: token rows gathered by pair, h out
+  CUtensorMap maps[7];
+  if (!fp8_maps(maps, w->gate_q, w->up_q, static_cast<int64_t>(E + S) * I, x, T, H)) return COLI_ERR_CUDA;
   g.a_s = x_scale;
+  g.w_s = w->gate_s;
+  g.w_s1 = w->up_s;
+  g.out = lay.hq;
+  g.out_s = lay.hs;
+  g.perm = perm;
   g.R = I;
-  g.K = H;
-  g.gather = 1;
-  const int blocks = std::min(P, E) + P / 64 + S * ((T + 63) / 64);
-  for (int m = 0; m < 2; ++m) {
-    g.w = m ? w->up_q : w->gate_q;
-    g.w_s = m ? w->up_s : w->gate_s;
-    g.out = m ? lay.up : lay.gate;
-    if (!launch(fp8_gemm_simple_kernel, dim3(blocks, (I + 63) / 64), dim3(256), 0, s, g)) return COLI_ERR_CUDA;
-  }
-  const long hb = static_cast<long>(P + S * T) * (I / kF8Block);
-  if (!launch(swiglu_fp8_kernel, dim3(static_cast<unsigned>(std::min<long>((hb + 7) / 8, 8L * di.sms))), dim3(256), 0,
-              s, static_cast<const float*>(lay.gate), static_cast<const float*>(lay.up), hb, lay.hq, lay.hs))
+  g.nk = H / kF8Block;
+  const int64_t tiles_gu = blocks_ub * (I / kF8Block);
+  if (!(few ? launch_fp8<2, 32, true>(maps, g, tiles_gu, 1, di.sms, s)
+            : launch_fp8<2, kF8Tokens, true>(maps, g, tiles_gu, 1, di.sms, s)))
     return COLI_ERR_CUDA;
-  g.a = lay.hq;
+  // down: h rows in pair order, y out
+  if (!fp8_maps(maps, w->down_q, nullptr, static_cast<int64_t>(E + S) * H, lay.hq, rows, I)) return COLI_ERR_CUDA;
   g.a_s = lay.hs;
-  g.w = w->down_q;
   g.w_s = w->down_s;
+  g.w_s1 = nullptr;
   g.out = lay.y;
+  g.out_s = nullptr;
+  g.out_f32 = 1;
+  g.perm = nullptr;
   g.R = H;
-  g.K = I;
-  g.gather = 0;
-  if (!launch(fp8_gemm_simple_kernel, dim3(blocks, (H + 63) / 64), dim3(256), 0, s, g)) return COLI_ERR_CUDA;
+  g.nk = I / kF8Block;
+  const int64_t tiles_dn = blocks_ub * (H / kF8Block);
+  if (!(few ? launch_fp8<1, 32, false>(maps, g, tiles_dn, 1, di.sms, s)
+            : launch_fp8<2, kF8Tokens, false>(maps, g, (tiles_dn + 1) / 2, 1, di.sms, s)))
+    return COLI_ERR_CUDA;
   const long work = static_cast<long>(T) * (H / 4);
   return launch(combine_kernel, dim3(static_cast<unsigned>(std::min<long>((work + 255) / 256, 16L * di.sms))), dim3(256),
                 0, s, static_cast<const float*>(lay.y), pair_pos, topk_w, residual, T, k, S, H, out,
