@@ -6,29 +6,31 @@
 // rows x 128 columns.  Each block's products are summed in fp32, then scaled and
 // added to the fp32 total in block order.
 //
-// One tcgen05 kernel does every product.  The weights are the MMA's A operand
-// (128 rows = one row of weight scales), the tokens its N side (up to NT of them,
-// rounded up to 16), so that a batch of one token costs no more tensor work than
-// 16 and an expert's tokens are never padded to 128.  A tile is NMAT blocks of
-// 128 weight rows x up to NT tokens: gate and up blocks of the same 128 columns of
-// h, or neighbouring blocks of one matrix.  Per 128-wide K block:
+// One tcgen05 kernel does every product.  The tokens are the MMA's A operand (128
+// rows of tensor memory, a thread's lane = a token), NMAT blocks of 128 weight
+// rows its N side: the scale of a K block is then one number per thread and
+// weight block, the token's scale times the block's, kept in a register.  (With
+// the weights as A a thread needs a scale per column: the 32 loads from shared
+// memory per K block made the product 2.4 times slower than the tensor pipe.)  A
+// tile is up to NT tokens x NMAT * 128 weight rows: gate and up blocks of the same
+// 128 columns of h, or neighbouring blocks of one matrix.  Per 128-wide K block:
 //   * warp 0 brings the weight blocks (128 x 128 bytes each) and the token rows
 //     into a stage of shared memory by TMA (128B swizzle); rows of a routed segment
 //     are gathered four at a time by their token index, so the batch is never
 //     copied into pair order;
-//   * one thread of warp 1 multiplies each weight block with the tokens (four
-//     tcgen05.mma kind::f8f6f4, K = 32 each) into a slot of tensor memory, a fresh
-//     accumulator per K block;
-//   * warps 2 and 3 write the slot's token scales times its weight scale to shared
-//     memory;
+//   * warp 1 multiplies them (four tcgen05.mma kind::f8f6f4, K = 32 each) into a
+//     slot of tensor memory, a fresh accumulator per K block;
 //   * warps 4..11 read the slot (tcgen05.ld), multiply-add it into fp32 totals in
-//     registers (fma.rn.f32x2: two columns an instruction) and free the slot.
-// A thread of warps 4..11 owns one weight row and every other 16-token chunk: 160
-// totals for 2 x 160 tokens, hence the register split below.
-// The gate/up launch ends a tile with h = silu(g) u, the row block's maximum over
-// its 128 columns (one redux per warp and token, four warps through shared
-// memory) and e4m3 codes with their scale: g and u never leave the SM.
+//     registers and free the slot.  A thread owns one token and half of the
+//     columns: 128 totals, hence the register split below.
+// The gate/up launch ends a tile with h = silu(g) u, the token's maximum over the
+// tile's 128 columns (two threads, through shared memory) and e4m3 codes with
+// their scale: g and u never leave the SM.
+// A operand rows past the tile's tokens are whatever shared memory holds; they
+// only reach tensor-memory lanes that nothing reads.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 #include "k_ffn_prefill.cuh"
 #include "k_norm_fp8.cuh"
@@ -36,7 +38,7 @@
 namespace coli {
 
 constexpr int kF8MaxSeg = 1024 + 8;   // unique routed + shared segments
-constexpr int kF8Threads = 384;       // warp 0 TMA, warp 1 MMA, warps 2 and 3 scales, warps 4..11 totals
+constexpr int kF8Threads = 384;       // warp 0 TMA, warp 1 MMA, warps 4..11 totals
 constexpr int kF8MaxSplit = 8;        // CTAs of a cluster that share a tile's K
 
 // What a launch multiplies: one dense product (seg_off NULL), or the segments of
@@ -61,31 +63,70 @@ struct F8Args {
 template <int NMAT, int NT>
 struct F8Cfg {
   static constexpr int WSTAGE = NMAT * 128 * 128;
-  static constexpr int STAGE = WSTAGE + NT * 128;
-  static constexpr int NSLOT = NT > 128 ? 3 : NT > 64 ? 4 : 8;      // accumulators in tensor memory
-  static constexpr int CH = 16;                                     // columns of a chunk
-  static constexpr int NCH = (NT / CH + 1) / 2;                     // chunks of a thread
-  static constexpr int META_INTS = 3 * kF8MaxSeg + 4;
-  static constexpr int FIXED = NSLOT * NT * 4 + 4 * NT * 4 + META_INTS * 4 + 512;
-  static constexpr int NST = (232448 - 1024 - FIXED) / STAGE;
-  static constexpr size_t SMEM = 1024 + static_cast<size_t>(NST) * STAGE + FIXED;
-  static_assert(NT % 16 == 0 && NT <= 256 && NSLOT * NT <= 512, "tensor memory budget");
-  static_assert(NST >= 3 && 2 * NST + 2 * NSLOT + 1 <= 60, "stages");
-  static_assert(STAGE % 1024 == 0, "stage alignment");
-  static_assert(NMAT * 128 * NT * 4 <= NST * STAGE, "split-K totals fit the stages");
+  static constexpr int ASTAGE = NT * 128;
+  static constexpr int SLOT = NMAT * 128;                           // tensor-memory columns of a K block
+  static constexpr int NSLOT = 512 / SLOT;
+  static constexpr int META_INTS = 2 * kF8MaxSeg + 4 + kF8MaxSeg / 2;
+  static constexpr int FIXED = 4 * 128 * 4 + META_INTS * 4 + 512;
+  static constexpr int NST = (232448 - 1024 - FIXED) / (WSTAGE + ASTAGE);
+  static constexpr size_t SMEM = 1024 + static_cast<size_t>(NST) * (WSTAGE + ASTAGE) + FIXED;
+  static constexpr int TOT_LD = NT + 1;                             // split K: totals [column][TOT_LD]
+  static_assert(NT % 32 == 0 && NT <= 128, "a tile's tokens are tensor-memory lanes");
+  static_assert(NST >= 3 && 2 * NST + 2 * NSLOT + 5 <= 60, "stages");
+  // the A operand's descriptor spans 128 rows whatever NT: the weight stages that
+  // follow the token stages keep that inside the allocation
+  static_assert(NST * WSTAGE >= 128 * 128 && ASTAGE % 1024 == 0, "operand extent");
+  static_assert(SLOT * TOT_LD * 4 <= NST * (WSTAGE + ASTAGE), "split-K totals fit the stages");
 };
 
 // ------------------------------------------------------------------ PTX --
 
-// D[128 x N] (+)= A[128 x 32] * B[N x 32]^T of e4m3, both K-major in shared memory.
+// D[128 x N] (+)= A[128 x 32] * B[N x 32]^T of e4m3, both K-major in shared memory,
+// issued by the lane whose `on` is not 0 (a predicate instead of a branch keeps
+// the descriptors warp-uniform).
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
+                                          uint32_t accumulate, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+
+// tc_commit by the lane whose `on` is not 0.
+__device__ __forceinline__ void tc_commit_on(uint64_t* bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(on)
+      : "memory");
+}
+
+// Whether the phase with this parity is complete, without waiting; the same answer in every lane.
+__device__ __forceinline__ bool warp_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
       : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // Four rows (y0..y3) of a 2-D map whose box is one row, 128 bytes from column x.
@@ -97,30 +138,26 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+// 32 columns of this warp's lane quarter.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr));
 }
 
-// Two fp32 totals as one 64-bit register pair: t = fma(d, s, t) in each half.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ void fma2(f32x2& t, uint32_t d0, uint32_t d1, f32x2 s) {
-  f32x2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(t) : "l"(d), "l"(s));
-}
-__device__ __forceinline__ float2 unpack2(f32x2 t) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(t));
-  return f;
-}
-__device__ __forceinline__ void lds_2x64(uint32_t addr, f32x2& a, f32x2& b) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+// Waits for this thread's tensor-memory loads; the registers pass through, so
+// that nothing that uses them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -139,18 +176,13 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-// Barrier of the four warps of one column half (128 threads), id 1 or 2.
-__device__ __forceinline__ void half_barrier(int half) {
-  asm volatile("bar.sync %0, 128;" ::"r"(half + 1) : "memory");
-}
-
 // ----------------------------------------------------------------- tiles --
 
 struct F8Tile {
   int e;        // expert (dense: 0)
   int rblk;     // tile of NMAT * 128 output columns (gate/up: of 128)
   int ntok;     // tokens
-  int npad;     // rounded up to 16
+  int npad;     // rows copied: rounded up to 16
   int arow;     // first token row, or first pair of a gathered segment
   int orow;     // first output row
   bool gather;
@@ -160,7 +192,7 @@ struct F8Tile {
 // tokens and, across the blocks of an expert, the same weights from L2.
 template <int NT>
 __device__ __forceinline__ F8Tile f8_tile(const F8Args& a, const int32_t* blk_off, const int32_t* seg,
-                                          const int32_t* uniq, int n_seg, int U, int mbk, int t) {
+                                          const uint16_t* uniq, int n_seg, int U, int mbk, int t) {
   F8Tile ti;
   const int blk = t / mbk;
   ti.rblk = t - blk * mbk;
@@ -207,6 +239,38 @@ __device__ __forceinline__ int f8_row(const F8Args& a, const F8Tile& ti, int n) 
   return ti.gather ? __ldg(a.perm + ti.arow + c) / a.k : ti.arow + c;
 }
 
+// N values of one output row from column col on, as 16-byte stores where rows and
+// columns allow it.
+template <int N>
+__device__ __forceinline__ void f8_store_row(const F8Args& a, size_t row, int col, const float (&v)[N]) {
+  const int left = a.R - col;
+  if (a.out_f32) {
+    float* o = static_cast<float*>(a.out) + row * a.R + col;
+    if (a.R % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        if (i < left) *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) o[i] = v[i];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + row * a.R + col;
+    if (a.R % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 8)
+        if (i < left)
+          *reinterpret_cast<uint4*>(o + i) = make_uint4(bf16x2(v[i], v[i + 1]), bf16x2(v[i + 2], v[i + 3]),
+                                                        bf16x2(v[i + 4], v[i + 5]), bf16x2(v[i + 6], v[i + 7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < left) o[i] = float_to_bf16_bits(v[i]);
+    }
+  }
+}
+
 // ------------------------------------------------------------ the kernel --
 
 // GU: the gate/up launch (NMAT = 2).  gridDim.x: the tiles' CTAs, or with clusters
@@ -222,17 +286,19 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   using C = F8Cfg<NMAT, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  float* sc_base = reinterpret_cast<float*>(smem + C::NST * C::STAGE);    // [NSLOT][NT]
-  float* red = sc_base + C::NSLOT * NT;                                   // [4][NT]: row-block maxima
-  int32_t* blk_off = reinterpret_cast<int32_t*>(red + 4 * NT);
-  int32_t* uniq = blk_off + kF8MaxSeg + 2;
-  int32_t* seg = uniq + kF8MaxSeg;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(red + 4 * NT + C::META_INTS);
+  uint8_t* a_stages = smem;                                              // token rows
+  uint8_t* w_stages = smem + C::NST * C::ASTAGE;                         // weight rows
+  float* red = reinterpret_cast<float*>(w_stages + C::NST * C::WSTAGE);  // [2 parities][2 halves][128]: maxima
+  int32_t* blk_off = reinterpret_cast<int32_t*>(red + 4 * 128);
+  int32_t* seg = blk_off + kF8MaxSeg + 2;
+  uint16_t* uniq = reinterpret_cast<uint16_t*>(seg + kF8MaxSeg + 2);      // expert ids below 1024
+  uint64_t* bars = reinterpret_cast<uint64_t*>(blk_off + C::META_INTS);
   uint64_t* full = bars;
   uint64_t* empty = full + C::NST;
   uint64_t* slot_full = empty + C::NST;
   uint64_t* slot_empty = slot_full + C::NSLOT;
-  uint64_t* mma_done = slot_empty + C::NSLOT;
+  uint64_t* pair_bar = slot_empty + C::NSLOT;      // [4]: the two warps of a lane quarter
+  uint64_t* mma_done = pair_bar + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* scratch = reinterpret_cast<int*>(red);     // 33 ints, before the tiles
@@ -244,9 +310,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(&empty[q], 1);
     }
     for (int q = 0; q < C::NSLOT; ++q) {
-      mbar_init(&slot_full[q], 3);      // the MMAs' commit and the two scale warps
+      mbar_init(&slot_full[q], 1);
       mbar_init(&slot_empty[q], 8);
     }
+    for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 2);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -264,7 +331,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // token blocks of every segment, each of near-equal parts of at most NT tokens
     U = __ldg(a.n_unique);
     n_seg = U + a.S;
-    for (int i = threadIdx.x; i < U; i += blockDim.x) uniq[i] = __ldg(a.unique_ids + i);
+    for (int i = threadIdx.x; i < U; i += blockDim.x) uniq[i] = static_cast<uint16_t>(__ldg(a.unique_ids + i));
     for (int i = threadIdx.x; i <= U; i += blockDim.x) seg[i] = __ldg(a.seg_off + i);
     __syncthreads();
     int base = 0;
@@ -297,7 +364,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   auto tile_at = [&](int t) { return f8_tile<NT>(a, blk_off, seg, uniq, n_seg, U, mbk, t); };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ----------------------------------------------------- TMA producer
       // the rows may come from an earlier kernel's plain stores
@@ -308,20 +375,17 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         const F8Tile ti = tile_at(t);
         const int row0 = ti.e * a.R + ti.rblk * ROWS;
         // gathered rows: lane l takes rows 4l..4l+3 and 4(l+32)..: NT <= 256
-        int4 y0 = make_int4(0, 0, 0, 0), y1 = y0;
+        int4 y0 = make_int4(0, 0, 0, 0);
         if (ti.gather) {
           if (4 * lane < ti.npad)
             y0 = make_int4(f8_row(a, ti, 4 * lane), f8_row(a, ti, 4 * lane + 1), f8_row(a, ti, 4 * lane + 2),
                            f8_row(a, ti, 4 * lane + 3));
-          if (NT > 128 && 4 * (lane + 32) < ti.npad)
-            y1 = make_int4(f8_row(a, ti, 4 * lane + 128), f8_row(a, ti, 4 * lane + 129),
-                           f8_row(a, ti, 4 * lane + 130), f8_row(a, ti, 4 * lane + 131));
         }
         for (int kb = kb0; kb < kb1; ++kb, ++st) {
           const int s = static_cast<int>(st % C::NST);
           if (!(ok = warp_wait(&empty[s], ((st / C::NST) & 1u) ^ 1u, abort_flag, a.status))) break;
-          uint8_t* dst = smem + s * C::STAGE;
-          uint8_t* bdst = dst + C::WSTAGE;
+          uint8_t* dst = w_stages + s * C::WSTAGE;
+          uint8_t* bdst = a_stages + s * C::ASTAGE;
           if (lane == 0) {
             mbar_arrive_expect_tx(&full[s], C::WSTAGE + ti.npad * 128);
             tma_load_2d(dst, &mw0, &full[s], kb * 128, row0);
@@ -338,8 +402,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           __syncwarp();
           if (ti.gather) {
             if (4 * lane < ti.npad) tma_gather4(bdst + lane * 512, &mgat, &full[s], kb * 128, y0);
-            if (NT > 128 && 4 * (lane + 32) < ti.npad)
-              tma_gather4(bdst + (lane + 32) * 512, &mgat, &full[s], kb * 128, y1);
           }
         }
       }
@@ -352,104 +414,48 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issue
-      if (lane == 0) {
-        uint32_t st = 0, sl = 0;
-        bool ok = true;
-        for (int t = t_first; ok && t < tiles; t += t_step) {
-          const F8Tile ti = tile_at(t);
-          const uint32_t idesc = idesc_f16_m128(ti.npad);     // e4m3 has type field 0 too
-          for (int kb = kb0; ok && kb < kb1; ++kb, ++st) {
-            const int s = static_cast<int>(st % C::NST);
-            if (!(ok = mbar_wait(&full[s], (st / C::NST) & 1u, abort_flag, a.status))) break;
-            const uint32_t ws = smem_addr(smem + s * C::STAGE), bs = ws + C::WSTAGE;
+      // The whole warp walks the loop, so that addresses and descriptors stay
+      // warp-uniform; one elected lane issues.  An MMA of 128 x 256 x 32 takes 128
+      // cycles and its issue waits for the one before it, so a wait between two
+      // MMAs leaves the tensor pipe idle: the barriers of the next K block are
+      // looked at before the last MMA of this one.
+      const uint32_t leader = elect_one();
+      int s = 0, q = 0;
+      uint32_t sph = 0, qph = 1;              // phases: stage filled, slot freed
+      const uint64_t wdesc0 = sw128_kmajor_desc(smem_addr(w_stages));
+      const uint64_t adesc0 = sw128_kmajor_desc(smem_addr(a_stages));
+      const uint32_t idesc = idesc_f16_m128(NMAT * 128);     // e4m3 has type field 0 too
+      bool ok = true, stage_ready = false, slot_ready = false;
+      for (int t = t_first; ok && t < tiles; t += t_step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!stage_ready && !(ok = warp_wait(&full[s], sph, abort_flag, a.status))) break;
+          if (!slot_ready && !(ok = warp_wait(&slot_empty[q], qph, abort_flag, a.status))) break;
+          tc_fence_after();
+          const uint64_t wdesc = wdesc0 + static_cast<uint64_t>(s * (C::WSTAGE / 16));
+          const uint64_t adesc = adesc0 + static_cast<uint64_t>(s * (C::ASTAGE / 16));
+          const int s1 = s + 1 == C::NST ? 0 : s + 1, q1 = q + 1 == C::NSLOT ? 0 : q + 1;
+          const uint32_t sph1 = s1 ? sph : sph ^ 1u, qph1 = q1 ? qph : qph ^ 1u;
 #pragma unroll
-            for (int m = 0; m < NMAT; ++m, ++sl) {
-              const int q = static_cast<int>(sl % C::NSLOT);
-              if (!(ok = mbar_wait(&slot_empty[q], ((sl / C::NSLOT) & 1u) ^ 1u, abort_flag, a.status))) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f8_ss(tbase + q * NT, sw128_kmajor_desc(ws + m * 128 * 128 + kk * 32),
-                          sw128_kmajor_desc(bs + kk * 32), idesc, kk != 0);
-              tc_commit(&slot_full[q]);
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk == 3) {
+              stage_ready = warp_test(&full[s1], sph1);
+              slot_ready = warp_test(&slot_empty[q1], qph1);
             }
-            if (!ok) break;
-            tc_commit(&empty[s]);
+            mma_f8_ss(tbase + q * C::SLOT, adesc + kk * 2, wdesc + kk * 2, idesc, kk != 0, leader);
           }
+          tc_commit_on(&slot_full[q], leader);
+          tc_commit_on(&empty[s], leader);
+          s = s1;
+          sph = sph1;
+          q = q1;
+          qph = qph1;
         }
-        // every MMA of this CTA has completed before TMEM is released
+      }
+      // every MMA of this CTA has completed before TMEM is released
+      if (leader) {
         int dummy = 0;
         tc_commit(mma_done);
         mbar_wait(mma_done, 0, reinterpret_cast<volatile int*>(&dummy), a.status);
-      }
-      __syncwarp();
-    } else {
-      // ----------------------------------------------------------- scales
-      // Both warps serve every slot, each its 32 of every 64 columns (a warp that
-      // skipped slots could run a whole barrier phase ahead of the others).  The
-      // next four K blocks' scales, of the next tile at a tile's end, are loaded
-      // while four are in use.
-      constexpr int NI = (NT + 63) / 64;
-      const int c0 = lane + 32 * (warp - 2);
-      const float* ap[NI];
-      const float* wp[NMAT];
-      float av[NI][4], wv[NMAT][4], an[NI][4], wn[NMAT][4];
-      auto set_tile = [&](int t) {
-        const F8Tile ti = tile_at(t);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) ap[i] = a.a_s + static_cast<size_t>(f8_row(a, ti, c0 + 64 * i)) * a.nk;
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m) {
-          const int rb = GU ? ti.rblk : min(ti.rblk * NMAT + m, nrb - 1);
-          wp[m] = (GU && m ? a.w_s1 : a.w_s) + (static_cast<size_t>(ti.e) * nrb + rb) * a.nk;
-        }
-      };
-      auto load = [&](int g) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int kb = min(g + c, kb1 - 1);
-#pragma unroll
-          for (int i = 0; i < NI; ++i) an[i][c] = __ldg(ap[i] + kb);
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m) wn[m][c] = __ldg(wp[m] + kb);
-        }
-      };
-      uint32_t sl = 0;
-      bool ok = true;
-      if (t_first < tiles) {
-        set_tile(t_first);
-        load(kb0);
-      }
-      for (int t = t_first; ok && t < tiles; t += t_step) {
-        for (int g = kb0; ok && g < kb1; g += 4) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-#pragma unroll
-            for (int i = 0; i < NI; ++i) av[i][c] = an[i][c];
-#pragma unroll
-            for (int m = 0; m < NMAT; ++m) wv[m][c] = wn[m][c];
-          }
-          if (g + 4 < kb1) {
-            load(g + 4);
-          } else if (t + t_step < tiles) {
-            set_tile(t + t_step);
-            load(kb0);
-          }
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (g + c >= kb1 || !ok) break;
-#pragma unroll
-            for (int m = 0; m < NMAT; ++m, ++sl) {
-              const int q = static_cast<int>(sl % C::NSLOT);
-              if (!(ok = warp_wait(&slot_empty[q], ((sl / C::NSLOT) & 1u) ^ 1u, abort_flag, a.status))) break;
-#pragma unroll
-              for (int i = 0; i < NI; ++i)
-                if (c0 + 64 * i < NT) sc_base[q * NT + c0 + 64 * i] = av[i][c] * wv[m][c];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&slot_full[q]);
-            }
-          }
-        }
       }
       __syncwarp();
     }
@@ -461,153 +467,178 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
   } else {
     // ------------------------------------------------------------- totals
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int q4 = warp & 3;                   // TMEM lane quarter
-    const int half = (warp - 4) >> 2;          // chunks half, half + 2, ...
-    const int r = 32 * q4 + lane;              // weight row within a 128-row block
-    const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q4) << 16);
-    uint32_t sl = 0;
+    const int half = (warp - 4) >> 2;          // columns half * 64 .. + 63 of each 128
+    const int r = 32 * q4 + lane;              // token of the tile
+    const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q4) << 16) + half * 64;
+    int q = 0;
+    uint32_t qph = 0, met = 0;
     bool ok = true;
+    float acc[NMAT][2][32];
     for (int t = t_first; ok && t < tiles; t += t_step) {
       const F8Tile ti = tile_at(t);
-      const int nch = ti.npad >> 4;
-      f32x2 acc[NMAT][C::NCH][8];
+      const bool any = 32 * q4 < ti.ntok;      // this warp's lanes hold tokens
+      // the token's and the weight blocks' scales, two K blocks at a time, the next
+      // two on their way
+      const float* ap = a.a_s + static_cast<size_t>(f8_row(a, ti, r)) * a.nk;
+      const float* wp[NMAT];
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) {
+        const int rb = GU ? ti.rblk : min(ti.rblk * NMAT + m, nrb - 1);
+        wp[m] = (GU && m ? a.w_s1 : a.w_s) + (static_cast<size_t>(ti.e) * nrb + rb) * a.nk;
+      }
+      float an[2], wn[NMAT][2];
+      auto load_scales = [&](int g) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int kb = min(g + c, kb1 - 1);
+          an[c] = __ldg(ap + kb);
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m) wn[m][c] = __ldg(wp[m] + kb);
+        }
+      };
+      if (any) load_scales(kb0);
 #pragma unroll
       for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-        for (int c = 0; c < C::NCH; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[m][c][i] = 0ull;
-      for (int kb = kb0; ok && kb < kb1; ++kb) {
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m, ++sl) {
-          const int q = static_cast<int>(sl % C::NSLOT);
-          if (!(ok = warp_wait(&slot_full[q], (sl / C::NSLOT) & 1u, abort_flag, a.status))) break;
+          for (int i = 0; i < 32; ++i) acc[m][c][i] = 0.f;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&slot_empty[q]);
+        if (++q == C::NSLOT) {
+          q = 0;
+          qph ^= 1u;
+        }
+      };
+      if (!any) {
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
+          if (!(ok = warp_wait(&slot_full[q], qph, abort_flag, a.status))) break;
+          release();
+        }
+      } else {
+        // 32 columns are on their way from tensor memory (about 100 cycles) while
+        // 32 are added, the next slot's first ones too
+        uint32_t d[2][32];
+        auto fetch = [&](uint32_t (&into)[32]) -> bool {
+          if (!warp_wait(&slot_full[q], qph, abort_flag, a.status)) return false;
           tc_fence_after();
-          const uint32_t sca = smem_addr(sc_base + q * NT);
+          tmem_ld32(tq + q * C::SLOT, into);
+          return true;
+        };
+        ok = fetch(d[0]);
+        for (int g = kb0; ok && g < kb1; g += 2) {
+          float sc[NMAT][2];
 #pragma unroll
-          for (int c = 0; c < C::NCH; ++c) {
-            const int ch = 2 * c + half;
-            if (ch < nch) {
-              uint32_t d[16];
-              tmem_ld16(tq + q * NT + ch * 16, d);
-              f32x2 s[8];
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) lds_2x64(sca + ch * 64 + i * 16, s[2 * i], s[2 * i + 1]);
-              tmem_wait_ld();
+            for (int m = 0; m < NMAT; ++m) sc[m][c] = an[c] * wn[m][c];
+          if (g + 2 < kb1) load_scales(g + 2);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) fma2(acc[m][c][i], d[2 * i], d[2 * i + 1], s[i]);
+          for (int c = 0; c < 2; ++c) {
+            if (g + c >= kb1) break;
+            const uint32_t ta = tq + q * C::SLOT;
+#pragma unroll
+            for (int i = 0; i < 2 * NMAT; ++i) {
+              uint32_t(&cur)[32] = d[i & 1];
+              uint32_t(&nxt)[32] = d[(i + 1) & 1];
+              tmem_wait_ld32(cur);
+              if (i + 1 < 2 * NMAT) {
+                tmem_ld32(ta + (i + 1) / 2 * 128 + (i + 1) % 2 * 32, nxt);
+              } else {
+                release();
+                if (g + c + 1 < kb1 && !(ok = fetch(nxt))) break;
+              }
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                acc[i / 2][i % 2][x] = fmaf(__uint_as_float(cur[x]), sc[i / 2][c], acc[i / 2][i % 2][x]);
             }
+            if (!ok) break;
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&slot_empty[q]);
         }
       }
       if (!ok) break;
       if constexpr (GU) {
-        // h, the maximum of its 128 columns per token, codes and scale
-        float* rw = red + q4 * NT;
+        if (!any) continue;
+        // h, the maximum of the token's 128 columns (64 in each of two threads),
+        // codes and scale
+        float mx = 0.f;
 #pragma unroll
-        for (int c = 0; c < C::NCH; ++c) {
-          const int ch = 2 * c + half;
-          if (ch < nch) {
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 g = unpack2(acc[0][c][i]), u = unpack2(acc[1][c][i]);
-              const float h0 = g.x / (1.0f + expf(-g.x)) * u.x, h1 = g.y / (1.0f + expf(-g.y)) * u.y;
-              asm("mov.b64 %0, {%1, %2};" : "=l"(acc[0][c][i]) : "f"(h0), "f"(h1));
-              // magnitudes compare as unsigned integers, NaN above infinity
-              const uint32_t m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(h0) & 0x7fffffffu);
-              const uint32_t m1 = __reduce_max_sync(0xffffffffu, __float_as_uint(h1) & 0x7fffffffu);
-              if (lane == 0) {
-                rw[ch * 16 + 2 * i] = __uint_as_float(m0);
-                rw[ch * 16 + 2 * i + 1] = __uint_as_float(m1);
-              }
-            }
+          for (int i = 0; i < 32; ++i) {
+            const float g = acc[0][c][i];
+            const float h = __fdividef(g, 1.0f + expf(-g)) * acc[NMAT - 1][c][i];
+            acc[0][c][i] = h;
+            mx = max_nan(mx, fabsf(h));
           }
-        }
-        half_barrier(half);
-        uint8_t* hq = static_cast<uint8_t*>(a.out);
+        // the two warps of this lane quarter meet; with two sets of maxima a warp
+        // writes a set again only after its partner came to the meeting in between
+        float* rw = red + (met & 1u) * 256;
+        rw[half * 128 + r] = mx;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pair_bar[q4]);
+        if (!(ok = warp_wait(&pair_bar[q4], met & 1u, abort_flag, a.status))) break;
+        ++met;
+        mx = max_nan(mx, rw[(half ^ 1) * 128 + r]);
+        if (r < ti.ntok) {
+          float inv;
+          const float scl = f8_scale(mx, &inv);
+          const size_t row = static_cast<size_t>(ti.orow + r);
+          if (half == 0) a.out_s[row * nrb + ti.rblk] = scl;
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + row * a.R + ti.rblk * 128 + half * 64);
 #pragma unroll
-        for (int c = 0; c < C::NCH; ++c) {
-          const int ch = 2 * c + half;
-          if (ch < nch) {
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int n = ch * 16 + i;
-              if (n < ti.ntok) {
-                const float m = max_nan(max_nan(red[n], red[NT + n]), max_nan(red[2 * NT + n], red[3 * NT + n]));
-                float inv;
-                const float scl = f8_scale(m, &inv);
-                const float2 h = unpack2(acc[0][c][i >> 1]);
-                const size_t row = static_cast<size_t>(ti.orow + n);
-                hq[row * a.R + ti.rblk * 128 + r] =
-                    static_cast<uint8_t>(__nv_cvt_float_to_fp8((i & 1 ? h.y : h.x) * inv, __NV_SATFINITE, __NV_E4M3));
-                if (r == 0) a.out_s[row * nrb + ti.rblk] = scl;
+            for (int x = 0; x < 2; ++x) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float* h = &acc[0][c][16 * x + 4 * y];
+                w[y] = f8x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
               }
+              dst[2 * c + x] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          }
         }
-        half_barrier(half);      // the maxima have been read
       } else if (split == 1) {
+        if (r < ti.ntok) {
 #pragma unroll
-        for (int m = 0; m < NMAT; ++m) {
-          const int col = ti.rblk * ROWS + m * 128 + r;
-          if (col < a.R) {
+          for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-            for (int c = 0; c < C::NCH; ++c) {
-              const int ch = 2 * c + half;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int n = ch * 16 + i;
-                if (n < ti.ntok) {
-                  const float2 v = unpack2(acc[m][c][i >> 1]);
-                  const float y = i & 1 ? v.y : v.x;
-                  const size_t at = static_cast<size_t>(ti.orow + n) * a.R + col;
-                  if (a.out_f32)
-                    static_cast<float*>(a.out)[at] = y;
-                  else
-                    static_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(y);
-                }
-              }
+            for (int c = 0; c < 2; ++c) {
+              const int col = ti.rblk * ROWS + m * 128 + half * 64 + c * 32;
+              f8_store_row<32>(a, static_cast<size_t>(ti.orow + r), col, acc[m][c]);
             }
-          }
         }
-      } else {
+      } else if (r < NT) {
         // split K: totals to shared memory (every copy and MMA of this CTA is done:
-        // its last slot was full), [column][NMAT * 128] so that lanes are neighbours
+        // its last slot was full)
         float* tot = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-          for (int c = 0; c < C::NCH; ++c) {
-            const int ch = 2 * c + half;
-            if (ch < nch) {
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 v = unpack2(acc[m][c][i]);
-                tot[(ch * 16 + 2 * i) * (NMAT * 128) + m * 128 + r] = v.x;
-                tot[(ch * 16 + 2 * i + 1) * (NMAT * 128) + m * 128 + r] = v.y;
-              }
-            }
-          }
+            for (int i = 0; i < 32; ++i) tot[(m * 128 + half * 64 + c * 32 + i) * C::TOT_LD + r] = acc[m][c][i];
       }
     }
     if (split > 1) {
       cluster_arrive();
       cluster_wait();
       if (ok && t_first < tiles) {
-        // this CTA adds its share of the columns over the ranks, in rank order
+        // this CTA adds its share of the tokens over the ranks, in rank order
         const F8Tile ti = tile_at(t_first);
         const int x = threadIdx.x - 128;
-        constexpr int PER = 256 / (NMAT * 128);           // columns at a time
-        const int row = x % (NMAT * 128);
-        const int col = ti.rblk * ROWS + row;
+        constexpr int PER = 256 / (NMAT * 128);           // tokens at a time
+        const int c = x % (NMAT * 128);
+        const int col = ti.rblk * ROWS + c;
         const uint32_t base = smem_addr(smem);
         for (int n = rank * PER + x / (NMAT * 128); n < ti.ntok; n += split * PER) {
           float y = 0.f;
-          for (int c = 0; c < split; ++c) y += ld_cluster_f32(base + (n * (NMAT * 128) + row) * 4, c);
+          for (int p = 0; p < split; ++p) y += ld_cluster_f32(base + (c * C::TOT_LD + n) * 4, p);
           if (col < a.R) {
             const size_t at = static_cast<size_t>(ti.orow + n) * a.R + col;
             if (a.out_f32)
