@@ -103,11 +103,12 @@ bool fp8_kernel_ready() {
          cudaFuncGetAttributes(&at, fp8_gemm_kernel<NMAT, NT, GU>) == cudaSuccess && at.numRegs >= 168;
 }
 
-constexpr int kF8Tokens = 128;   // tokens of a tile of the 8-bit product when there are more than 32
+constexpr int kF8Few = 32;       // tokens of a tile of the 8-bit product in small batches
+constexpr int kF8Tokens = 128;   // and in larger ones
 
 bool fp8_kernels_ready() {
-  return fp8_kernel_ready<2, 32, true>() && fp8_kernel_ready<2, kF8Tokens, true>() && fp8_kernel_ready<2, 32, false>() &&
-         fp8_kernel_ready<2, kF8Tokens, false>() && fp8_kernel_ready<1, 32, false>() &&
+  return fp8_kernel_ready<2, kF8Few, true>() && fp8_kernel_ready<2, kF8Tokens, true>() && fp8_kernel_ready<2, kF8Few, false>() &&
+         fp8_kernel_ready<2, kF8Tokens, false>() && fp8_kernel_ready<1, kF8Few, false>() &&
          fp8_kernel_ready<1, kF8Tokens, false>();
 }
 

@@ -53,10 +53,12 @@ struct F8Args {
   uint32_t* status;
   int M, R, nk;            // dense rows; output columns of one expert; K blocks
   int out_f32;
+  int wide;                // fp32 rows start on 32-byte boundaries
   const int32_t* unique_ids;
   const int32_t* n_unique;
   const int32_t* seg_off;
-  const int32_t* perm;     // gathered token rows: perm / k (NULL: the pair's own row)
+  const int32_t* perm;     // rows gathered by the copies: token perm / k of a pair (NULL: the pair's own row)
+  int shared_row;          // first token row of every shared expert; -1: each has rows of its own, as out has
   int T, k, E, S, P;
 };
 
@@ -64,19 +66,23 @@ template <int NMAT, int NT>
 struct F8Cfg {
   static constexpr int WSTAGE = NMAT * 128 * 128;
   static constexpr int ASTAGE = NT * 128;
-  static constexpr int SLOT = NMAT * 128;                           // tensor-memory columns of a K block
-  static constexpr int NSLOT = 512 / SLOT;
+  // A slot of tensor memory holds one weight block's product of a K block: four
+  // slots, freed one by one, but announced together: a commit drains the tensor
+  // pipe for about 80 cycles, so there is one per K block, and the barrier that it
+  // arrives on frees the stage for the copies and hands the slots to the totals.
+  static constexpr int SLOT = 128;
+  static constexpr int NSLOT = 4;
   static constexpr int META_INTS = 2 * kF8MaxSeg + 4 + kF8MaxSeg / 2;
   static constexpr int FIXED = 4 * 128 * 4 + META_INTS * 4 + 512;
   static constexpr int NST = (232448 - 1024 - FIXED) / (WSTAGE + ASTAGE);
   static constexpr size_t SMEM = 1024 + static_cast<size_t>(NST) * (WSTAGE + ASTAGE) + FIXED;
   static constexpr int TOT_LD = NT + 1;                             // split K: totals [column][TOT_LD]
   static_assert(NT % 32 == 0 && NT <= 128, "a tile's tokens are tensor-memory lanes");
-  static_assert(NST >= 3 && 2 * NST + 2 * NSLOT + 5 <= 60, "stages");
+  static_assert(NST >= 3 && 2 * NST + NSLOT + 5 <= 60 && NST > NSLOT / NMAT, "stages");
   // the A operand's descriptor spans 128 rows whatever NT: the weight stages that
   // follow the token stages keep that inside the allocation
   static_assert(NST * WSTAGE >= 128 * 128 && ASTAGE % 1024 == 0, "operand extent");
-  static_assert(SLOT * TOT_LD * 4 <= NST * (WSTAGE + ASTAGE), "split-K totals fit the stages");
+  static_assert(NMAT * 128 * TOT_LD * 4 <= NST * (WSTAGE + ASTAGE), "split-K totals fit the stages");
 };
 
 // ------------------------------------------------------------------ PTX --
@@ -160,6 +166,14 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
                  "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
 }
 
+// A load that stays where it is written (left to itself the compiler moves a
+// prefetch down to its use when registers are short).
+__device__ __forceinline__ float ldg_here(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -221,7 +235,7 @@ __device__ __forceinline__ F8Tile f8_tile(const F8Args& a, const int32_t* blk_of
       ti.e = a.E + (lo - U);
       cnt = a.T;
       obase = a.P + (lo - U) * a.T;
-      abase = a.perm ? 0 : obase;
+      abase = a.shared_row >= 0 ? a.shared_row : obase;
     }
   }
   const int start = static_cast<int>(static_cast<int64_t>(cnt) * j / nb);
@@ -239,6 +253,37 @@ __device__ __forceinline__ int f8_row(const F8Args& a, const F8Tile& ti, int n) 
   return ti.gather ? __ldg(a.perm + ti.arow + c) / a.k : ti.arow + c;
 }
 
+// The expert input of a routed batch in pair order: row i < P is the codes and
+// scales of token perm[i] / k, the `extra` rows after them
+// the tokens in order (T of them for the shared experts, or none).  One warp per row, 16-byte moves.  For more than 32 tokens
+// this pays: copies that gather four rows each bring 128 rows in 1800 cycles, a
+// plain 128-row copy in 1000 (gate/up of 4096 tokens 2.84 against 1.73 ms, and this
+// kernel takes 0.07).
+__global__ void __launch_bounds__(256) f8_gather_kernel(const uint8_t* __restrict__ x, const float* __restrict__ x_s,
+                                                        const int32_t* __restrict__ perm, int k, int P, int extra, int T, int H,
+                                                        uint8_t* __restrict__ xg, float* __restrict__ sg) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < P + extra; i += gridDim.x * 8) {
+    // a pair whose expert was out of range is in no segment: perm may not name it
+    const int t = i < P ? __ldg(perm + i) / k : i - P;
+    if (static_cast<unsigned>(t) >= static_cast<unsigned>(T)) continue;
+    const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * H);
+    uint4* dst = reinterpret_cast<uint4*>(xg + static_cast<size_t>(i) * H);
+    for (int c = lane; c < H / 16; c += 32) dst[c] = __ldg(src + c);
+    for (int c = lane; c < H / kF8Block; c += 32)
+      sg[static_cast<size_t>(i) * (H / kF8Block) + c] = __ldg(x_s + static_cast<size_t>(t) * (H / kF8Block) + c);
+  }
+}
+
+// Eight fp32 values as one 32-byte store (a whole sector of a row).
+__device__ __forceinline__ void st_f32x8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 // N values of one output row from column col on, as 16-byte stores where rows and
 // columns allow it.
 template <int N>
@@ -246,7 +291,11 @@ __device__ __forceinline__ void f8_store_row(const F8Args& a, size_t row, int co
   const int left = a.R - col;
   if (a.out_f32) {
     float* o = static_cast<float*>(a.out) + row * a.R + col;
-    if (a.R % 4 == 0) {
+    if (a.wide) {
+#pragma unroll
+      for (int i = 0; i < N; i += 8)
+        if (i < left) st_f32x8(o + i, &v[i]);
+    } else if (a.R % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < N; i += 4)
         if (i < left) *reinterpret_cast<float4*>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -294,9 +343,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint16_t* uniq = reinterpret_cast<uint16_t*>(seg + kF8MaxSeg + 2);      // expert ids below 1024
   uint64_t* bars = reinterpret_cast<uint64_t*>(blk_off + C::META_INTS);
   uint64_t* full = bars;
-  uint64_t* empty = full + C::NST;
-  uint64_t* slot_full = empty + C::NST;
-  uint64_t* slot_empty = slot_full + C::NSLOT;
+  uint64_t* done = full + C::NST;                 // the stage's MMAs are complete
+  uint64_t* slot_empty = done + C::NST;
   uint64_t* pair_bar = slot_empty + C::NSLOT;      // [4]: the two warps of a lane quarter
   uint64_t* mma_done = pair_bar + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -307,10 +355,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   if (threadIdx.x == 0) {
     for (int q = 0; q < C::NST; ++q) {
       mbar_init(&full[q], 1);
-      mbar_init(&empty[q], 1);
+      mbar_init(&done[q], 1);
     }
     for (int q = 0; q < C::NSLOT; ++q) {
-      mbar_init(&slot_full[q], 1);
       mbar_init(&slot_empty[q], 8);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 2);
@@ -383,7 +430,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         }
         for (int kb = kb0; kb < kb1; ++kb, ++st) {
           const int s = static_cast<int>(st % C::NST);
-          if (!(ok = warp_wait(&empty[s], ((st / C::NST) & 1u) ^ 1u, abort_flag, a.status))) break;
+          if (!(ok = warp_wait(&done[s], ((st / C::NST) & 1u) ^ 1u, abort_flag, a.status))) break;
           uint8_t* dst = w_stages + s * C::WSTAGE;
           uint8_t* bdst = a_stages + s * C::ASTAGE;
           if (lane == 0) {
@@ -415,40 +462,43 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issue
       // The whole warp walks the loop, so that addresses and descriptors stay
-      // warp-uniform; one elected lane issues.  An MMA of 128 x 256 x 32 takes 128
-      // cycles and its issue waits for the one before it, so a wait between two
-      // MMAs leaves the tensor pipe idle: the barriers of the next K block are
+      // warp-uniform; one elected lane issues.  The barriers of the next product are
       // looked at before the last MMA of this one.
       const uint32_t leader = elect_one();
       int s = 0, q = 0;
       uint32_t sph = 0, qph = 1;              // phases: stage filled, slot freed
       const uint64_t wdesc0 = sw128_kmajor_desc(smem_addr(w_stages));
       const uint64_t adesc0 = sw128_kmajor_desc(smem_addr(a_stages));
-      const uint32_t idesc = idesc_f16_m128(NMAT * 128);     // e4m3 has type field 0 too
+      const uint32_t idesc = idesc_f16_m128(128);     // e4m3 has type field 0 too
       bool ok = true, stage_ready = false, slot_ready = false;
       for (int t = t_first; ok && t < tiles; t += t_step) {
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
           if (!stage_ready && !(ok = warp_wait(&full[s], sph, abort_flag, a.status))) break;
-          if (!slot_ready && !(ok = warp_wait(&slot_empty[q], qph, abort_flag, a.status))) break;
-          tc_fence_after();
           const uint64_t wdesc = wdesc0 + static_cast<uint64_t>(s * (C::WSTAGE / 16));
           const uint64_t adesc = adesc0 + static_cast<uint64_t>(s * (C::ASTAGE / 16));
-          const int s1 = s + 1 == C::NST ? 0 : s + 1, q1 = q + 1 == C::NSLOT ? 0 : q + 1;
-          const uint32_t sph1 = s1 ? sph : sph ^ 1u, qph1 = q1 ? qph : qph ^ 1u;
+          const int s1 = s + 1 == C::NST ? 0 : s + 1;
+          const uint32_t sph1 = s1 ? sph : sph ^ 1u;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk == 3) {
-              stage_ready = warp_test(&full[s1], sph1);
-              slot_ready = warp_test(&slot_empty[q1], qph1);
+          for (int m = 0; m < NMAT; ++m) {
+            if (!slot_ready && !(ok = warp_wait(&slot_empty[q], qph, abort_flag, a.status))) break;
+            tc_fence_after();
+            const int q1 = (q + 1) % C::NSLOT;
+            const uint32_t qph1 = q1 ? qph : qph ^ 1u;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk == 3) {
+                if (m == NMAT - 1) stage_ready = warp_test(&full[s1], sph1);
+                slot_ready = warp_test(&slot_empty[q1], qph1);
+              }
+              mma_f8_ss(tbase + q * C::SLOT, adesc + kk * 2, wdesc + m * 1024 + kk * 2, idesc, kk != 0, leader);
             }
-            mma_f8_ss(tbase + q * C::SLOT, adesc + kk * 2, wdesc + kk * 2, idesc, kk != 0, leader);
+            q = q1;
+            qph = qph1;
           }
-          tc_commit_on(&slot_full[q], leader);
-          tc_commit_on(&empty[s], leader);
+          if (!ok) break;
+          tc_commit_on(&done[s], leader);
           s = s1;
           sph = sph1;
-          q = q1;
-          qph = qph1;
         }
       }
       // every MMA of this CTA has completed before TMEM is released
@@ -472,9 +522,20 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const int half = (warp - 4) >> 2;          // columns half * 64 .. + 63 of each 128
     const int r = 32 * q4 + lane;              // token of the tile
     const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q4) << 16) + half * 64;
-    int q = 0;
-    uint32_t qph = 0, met = 0;
+    int q = 0, s = 0;                          // next slot; stage of the next K block
+    uint32_t sph = 0, met = 0;
     bool ok = true;
+    // Waits for the next K block's products.  The MMAs run at most NSLOT / NMAT K
+    // blocks ahead, fewer than the stages: its barrier cannot be a phase further.
+    auto next_block = [&]() -> bool {
+      if (!warp_wait(&done[s], sph, abort_flag, a.status)) return false;
+      if (++s == C::NST) {
+        s = 0;
+        sph ^= 1u;
+      }
+      tc_fence_after();
+      return true;
+    };
     float acc[NMAT][2][32];
     for (int t = t_first; ok && t < tiles; t += t_step) {
       const F8Tile ti = tile_at(t);
@@ -493,9 +554,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int kb = min(g + c, kb1 - 1);
-          an[c] = __ldg(ap + kb);
+          an[c] = ldg_here(ap + kb);
 #pragma unroll
-          for (int m = 0; m < NMAT; ++m) wn[m][c] = __ldg(wp[m] + kb);
+          for (int m = 0; m < NMAT; ++m) wn[m][c] = ldg_here(wp[m] + kb);
         }
       };
       if (any) load_scales(kb0);
@@ -509,27 +570,16 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&slot_empty[q]);
-        if (++q == C::NSLOT) {
-          q = 0;
-          qph ^= 1u;
-        }
+        q = (q + 1) % C::NSLOT;
       };
       if (!any) {
-        for (int kb = kb0; ok && kb < kb1; ++kb) {
-          if (!(ok = warp_wait(&slot_full[q], qph, abort_flag, a.status))) break;
-          release();
-        }
+        for (int kb = kb0; kb < kb1 && (ok = next_block()); ++kb)
+          for (int m = 0; m < NMAT; ++m) release();
       } else {
-        // 32 columns are on their way from tensor memory (about 100 cycles) while
-        // 32 are added, the next slot's first ones too
+        // 32 columns are on their way from tensor memory while 32 are added, the
+        // next K block's first ones too
         uint32_t d[2][32];
-        auto fetch = [&](uint32_t (&into)[32]) -> bool {
-          if (!warp_wait(&slot_full[q], qph, abort_flag, a.status)) return false;
-          tc_fence_after();
-          tmem_ld32(tq + q * C::SLOT, into);
-          return true;
-        };
-        ok = fetch(d[0]);
+        if ((ok = next_block())) tmem_ld32(tq + q * C::SLOT, d[0]);
         for (int g = kb0; ok && g < kb1; g += 2) {
           float sc[NMAT][2];
 #pragma unroll
@@ -540,21 +590,22 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             if (g + c >= kb1) break;
-            const uint32_t ta = tq + q * C::SLOT;
 #pragma unroll
-            for (int i = 0; i < 2 * NMAT; ++i) {
-              uint32_t(&cur)[32] = d[i & 1];
-              uint32_t(&nxt)[32] = d[(i + 1) & 1];
-              tmem_wait_ld32(cur);
-              if (i + 1 < 2 * NMAT) {
-                tmem_ld32(ta + (i + 1) / 2 * 128 + (i + 1) % 2 * 32, nxt);
-              } else {
-                release();
-                if (g + c + 1 < kb1 && !(ok = fetch(nxt))) break;
+            for (int m = 0; m < NMAT; ++m) {
+              tmem_wait_ld32(d[0]);
+              tmem_ld32(tq + q * C::SLOT + 32, d[1]);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) acc[m][0][x] = fmaf(__uint_as_float(d[0][x]), sc[m][c], acc[m][0][x]);
+              tmem_wait_ld32(d[1]);
+              release();
+              if (m + 1 < NMAT) {
+                tmem_ld32(tq + q * C::SLOT, d[0]);
+              } else if (g + c + 1 < kb1) {
+                if (!(ok = next_block())) break;
+                tmem_ld32(tq + q * C::SLOT, d[0]);
               }
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                acc[i / 2][i % 2][x] = fmaf(__uint_as_float(cur[x]), sc[i / 2][c], acc[i / 2][i % 2][x]);
+              for (int x = 0; x < 32; ++x) acc[m][1][x] = fmaf(__uint_as_float(d[1][x]), sc[m][c], acc[m][1][x]);
             }
             if (!ok) break;
           }

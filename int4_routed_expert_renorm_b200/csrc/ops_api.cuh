@@ -70,6 +70,8 @@ coli_status check_dims_fp8(const coli_moe_dims* d) {
 }
 
 struct F8Ws {
+  uint8_t* xg;    // [P+T][H] codes of x in pair order, then token order (more than 32 tokens)
+  float* sg;      // [P+T][H/128]
   uint8_t* hq;    // [P+S*T][I] codes of h
   float* hs;      // [P+S*T][I/128]
   float* y;       // [P+S*T][H]
@@ -86,6 +88,9 @@ F8Ws fp8_layout(const coli_moe_dims* d, int T, void* base) {
     o += align256(bytes);
     return p;
   };
+  const size_t grows = T > kF8Few ? static_cast<size_t>(T) * (d->top_k + 1) : 0;
+  w.xg = static_cast<uint8_t*>(take(grows * H));
+  w.sg = static_cast<float*>(take(grows * (H / kF8Block) * 4));
   w.hq = static_cast<uint8_t*>(take(rows * I));
   w.hs = static_cast<float*>(take(rows * (I / kF8Block) * 4));
   w.y = static_cast<float*>(take(rows * H * 4));
@@ -253,21 +258,22 @@ coli_status coli_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
   g.R = N;
   g.nk = nk;
   g.out_f32 = (flags & COLI_FP8_OUT_F32) ? 1 : 0;
+  g.wide = N % 8 == 0 && aligned(out, 32);
   CUtensorMap maps[7];
   if (!fp8_maps(maps, w, nullptr, N, a, M, K)) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
-  const bool few = M <= 32;
+  const bool few = M <= kF8Few;
   const int64_t blocks = few ? 1 : (M + kF8Tokens - 1) / kF8Tokens;
   const int64_t tiles1 = blocks * nrb, tiles2 = blocks * ((nrb + 1) / 2);
   bool ok;
   if (tiles2 >= di.sms) {
-    ok = few ? launch_fp8<2, 32, false>(maps, g, tiles2, 1, di.sms, s)
+    ok = few ? launch_fp8<2, kF8Few, false>(maps, g, tiles2, 1, di.sms, s)
              : launch_fp8<2, kF8Tokens, false>(maps, g, tiles2, 1, di.sms, s);
   } else {
     // fewer tiles than SMs: single weight blocks, and several CTAs per tile
     int split = static_cast<int>(std::min<int64_t>({kF8MaxSplit, di.sms / tiles1, nk / 2}));
     if (split < 1) split = 1;
-    ok = few ? launch_fp8<1, 32, false>(maps, g, tiles1, split, di.sms, s)
+    ok = few ? launch_fp8<1, kF8Few, false>(maps, g, tiles1, split, di.sms, s)
              : launch_fp8<1, kF8Tokens, false>(maps, g, tiles1, split, di.sms, s);
   }
   return ok ? COLI_OK : COLI_ERR_CUDA;
@@ -311,23 +317,34 @@ coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims* dims, const coli_moe_we
   g.E = E;
   g.S = S;
   g.P = P;
-  const bool few = T <= 32;
-  const int nt = few ? 32 : kF8Tokens;
+  const bool few = T <= kF8Few;
+  const int nt = few ? kF8Few : kF8Tokens;
   const int64_t blocks_ub = static_cast<int64_t>(std::min(P, E)) + P / nt + static_cast<int64_t>(S) * (T / nt + 1);
   const int64_t rows = static_cast<int64_t>(P) + static_cast<int64_t>(S) * T;
   // gate and up: token rows gathered by pair, h out
   CUtensorMap maps[7];
-  if (!fp8_maps(maps, w->gate_q, w->up_q, static_cast<int64_t>(E + S) * I, x, T, H)) return COLI_ERR_CUDA;
-  g.a_s = x_scale;
+  if (few) {
+    if (!fp8_maps(maps, w->gate_q, w->up_q, static_cast<int64_t>(E + S) * I, x, T, H)) return COLI_ERR_CUDA;
+    g.a_s = x_scale;
+    g.perm = perm;
+    g.shared_row = 0;
+  } else {
+    const int64_t grows = static_cast<int64_t>(P) + (S ? T : 0);
+    if (!launch(f8_gather_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((grows + 7) / 8, 8L * di.sms))), dim3(256),
+                0, s, x, x_scale, perm, k, P, S ? T : 0, T, H, lay.xg, lay.sg) ||
+        !fp8_maps(maps, w->gate_q, w->up_q, static_cast<int64_t>(E + S) * I, lay.xg, grows, H))
+      return COLI_ERR_CUDA;
+    g.a_s = lay.sg;
+    g.shared_row = P;
+  }
   g.w_s = w->gate_s;
   g.w_s1 = w->up_s;
   g.out = lay.hq;
   g.out_s = lay.hs;
-  g.perm = perm;
   g.R = I;
   g.nk = H / kF8Block;
   const int64_t tiles_gu = blocks_ub * (I / kF8Block);
-  if (!(few ? launch_fp8<2, 32, true>(maps, g, tiles_gu, 1, di.sms, s)
+  if (!(few ? launch_fp8<2, kF8Few, true>(maps, g, tiles_gu, 1, di.sms, s)
             : launch_fp8<2, kF8Tokens, true>(maps, g, tiles_gu, 1, di.sms, s)))
     return COLI_ERR_CUDA;
   // down: h rows in pair order, y out
@@ -338,11 +355,13 @@ coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims* dims, const coli_moe_we
   g.out = lay.y;
   g.out_s = nullptr;
   g.out_f32 = 1;
+  g.wide = 1;
   g.perm = nullptr;
+  g.shared_row = -1;
   g.R = H;
   g.nk = I / kF8Block;
   const int64_t tiles_dn = blocks_ub * (H / kF8Block);
-  if (!(few ? launch_fp8<1, 32, false>(maps, g, tiles_dn, 1, di.sms, s)
+  if (!(few ? launch_fp8<1, kF8Few, false>(maps, g, tiles_dn, 1, di.sms, s)
             : launch_fp8<2, kF8Tokens, false>(maps, g, (tiles_dn + 1) / 2, 1, di.sms, s)))
     return COLI_ERR_CUDA;
   const long work = static_cast<long>(T) * (H / 4);
