@@ -25,8 +25,14 @@ def __getattr__(name):
         return importlib.import_module(f".{name}", __name__)
     for mod, names in _LAZY.items():
         if name in names:
-            return getattr(importlib.import_module(f".{mod}", __name__), name)
+            return _keep(name, getattr(importlib.import_module(f".{mod}", __name__), name))
     lib = importlib.import_module("._lib", __name__)
     if hasattr(lib, name):
-        return getattr(lib, name)
+        return _keep(name, getattr(lib, name))
     raise AttributeError(name)
+
+
+def _keep(name, value):
+    """Later look-ups of a resolved name do not come through __getattr__."""
+    globals()[name] = value
+    return value

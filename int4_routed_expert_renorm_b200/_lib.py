@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libcolimoe.so")
 
@@ -169,7 +171,6 @@ def _layer_sizes(dims, T: int, out, residual, logits_in, logits_out, topk_ids_ou
 
 def _stream(stream):
     if stream is None:
-        import torch
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -356,45 +357,62 @@ def coli_moe_get_status(stream=None):
 
 
 # ---- balance loss, 8-bit floating point ------------------------------------
+#
+# These calls are short (a few microseconds on the GPU for single tokens), so
+# their checks are written for few interpreter steps: one pass per tensor over
+# type, size, layout and device.
 
-def _rows(t, esize: int, name: str):
-    """The shape of a 2-D tensor of `esize`-byte elements."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs two dimensions")
-    if t.element_size() != esize:
-        raise ValueError(f"{name}: elements of {t.element_size()} bytes, the call needs {esize}")
-    return t.shape
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_U8 = (torch.uint8, torch.bool)
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
+_ANY = None
 
 
-def _place(*tensors):
-    """Pointers of dense device tensors (None -> NULL) that all live on the
-    current device: the call launches there, on its stream."""
-    out, dev = [], None
-    for t in tensors:
-        if t is not None:
-            if not t.is_cuda or not t.is_contiguous():
-                _ptr(t)
-            if dev is None:
-                dev = t.device.index
-                import torch
-                if dev != torch.cuda.current_device():
-                    raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-            elif t.device.index != dev:
-                raise ValueError(f"tensors on cuda:{dev} and cuda:{t.device.index}: one device is needed")
-        out.append(None if t is None else t.data_ptr())
+def _refuse(specs, dev):
+    """Why _args refused its arguments: types and sizes first, then layout and device."""
+    given = [x for x in specs if x[1] is not None]
+    for name, t, types, n, at_least in given:
+        if types is not None and t.dtype not in types:
+            names = " or ".join(str(x).replace("torch.", "") for x in types)
+            raise ValueError(f"{name}: {t.dtype}, the call needs {names}")
+        if n is not None and (t.numel() < n if at_least else t.numel() != n):
+            raise ValueError(f"{name}: {t.numel()} elements, the call needs {'at least ' if at_least else ''}{n}")
+    for name, t, *_ in given:
+        _ptr(t)
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: a tensor on {t.device}, but the current device is cuda:{dev}")
+    raise ValueError("no CUDA device is initialised")
+
+
+def _args(*specs):
+    """Data pointers of (name, tensor, types, elements, at_least) arguments (None
+    -> NULL): dense tensors of these types and sizes on the current device, where
+    the call launches."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    out = []
+    for name, t, types, n, at_least in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if ((types is not None and t.dtype not in types) or (n is not None and (t.numel() < n if at_least else t.numel() != n))
+                or not t.is_contiguous() or t.get_device() != dev or dev < 0):
+            _refuse(specs, dev)
+        out.append(t.data_ptr())
     return out
 
 
-def _dtypes(**named):
-    """Refuse tensors whose element type is not one of those given: named[x] = (tensor, types)."""
-    for name, (t, types) in named.items():
-        if t is not None and str(t.dtype) not in types:
-            raise ValueError(f"{name}: {t.dtype}, the call needs {' or '.join(x.replace('torch.', '') for x in types)}")
+def _raw_stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-_F32, _I32, _U8 = ("torch.float32",), ("torch.int32",), ("torch.uint8", "torch.bool")
-_BF16 = ("torch.bfloat16", "torch.int16", "torch.uint16")
-_E4M3 = ("torch.float8_e4m3fn", "torch.uint8", "torch.int8")
+def _rows(t, name: str):
+    """The shape of a 2-D tensor."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs two dimensions")
+    return t.shape
 
 
 def coli_moe_balance_workspace_bytes(t_max: int, n_experts: int) -> int:
@@ -404,20 +422,16 @@ def coli_moe_balance_workspace_bytes(t_max: int, n_experts: int) -> int:
 def coli_moe_balance(logits, bias, topk_ids, mask, counts, n_live, prob_mean, loss, ws, stream=None):
     """Per-expert counts, mean probabilities and the balance loss of a routed
     batch (see the header).  mask: None, or uint8/bool [T], 0 for padding."""
-    T, E = _rows(logits, 4, "logits")
-    k = _rows(topk_ids, 4, "topk_ids")[1]
-    _dtypes(logits=(logits, _F32), bias=(bias, _F32), topk_ids=(topk_ids, _I32), mask=(mask, _U8), counts=(counts, _I32),
-            n_live=(n_live, _I32), prob_mean=(prob_mean, _F32), loss=(loss, _F32))
-    _need(bias, E, 4, "bias")
-    _need(topk_ids, T * k, 4, "topk_ids")
-    _need(mask, T, 1, "mask")
-    _need(counts, E, 4, "counts")
-    _need(n_live, 1, 4, "n_live")
-    _need(prob_mean, E, 4, "prob_mean")
-    _need(loss, 1, 4, "loss")
-    p = _place(logits, bias, topk_ids, mask, counts, n_live, prob_mean, loss, ws)
-    _check(_lib.coli_moe_balance(p[0], p[1], p[2], p[3], T, E, k, p[4], p[5], p[6], p[7], p[8],
-                                 ws.numel() * ws.element_size(), _stream(stream)), "coli_moe_balance")
+    T, E = _rows(logits, "logits")
+    k = _rows(topk_ids, "topk_ids")[1]
+    p = _args(("logits", logits, _F32, None, False), ("bias", bias, _F32, E, False),
+              ("topk_ids", topk_ids, _I32, T * k, False), ("mask", mask, _U8, T, False),
+              ("counts", counts, _I32, E, False), ("n_live", n_live, _I32, 1, False),
+              ("prob_mean", prob_mean, _F32, E, False), ("loss", loss, _F32, 1, False), ("ws", ws, _ANY, None, False))
+    st = _lib.coli_moe_balance(p[0], p[1], p[2], p[3], T, E, k, p[4], p[5], p[6], p[7], p[8], ws.nbytes,
+                               _raw_stream(stream))
+    if st:
+        _check(st, "coli_moe_balance")
 
 
 def coli_moe_balance_backward(logits, bias, mask, counts, n_live, grad_loss, topk_ids, topk_w, d_topk_w, d_logits,
@@ -425,65 +439,51 @@ def coli_moe_balance_backward(logits, bias, mask, counts, n_live, grad_loss, top
     """Gradient of the router logits from the balance loss and from the
     renormalised weights (see the header).  grad_loss: a device tensor of one
     fp32 value, or None; d_topk_w: the weights' gradient, or None."""
-    T, E = _rows(logits, 4, "logits")
+    T, E = _rows(logits, "logits")
     if d_topk_w is not None and (topk_ids is None or topk_w is None):
         raise ValueError("d_topk_w needs topk_ids and topk_w")
-    given = next((t for t in (topk_ids, topk_w, d_topk_w) if t is not None), None)
-    k = _rows(given, 4, "topk_ids")[1] if given is not None else None
-    if k is None:
+    given = topk_ids if topk_ids is not None else topk_w
+    if given is None:
         raise ValueError("topk_ids: the call needs the routing's shape [T, k]")
-    _dtypes(logits=(logits, _F32), bias=(bias, _F32), topk_ids=(topk_ids, _I32), mask=(mask, _U8), counts=(counts, _I32),
-            n_live=(n_live, _I32), grad_loss=(grad_loss, _F32), topk_w=(topk_w, _F32), d_topk_w=(d_topk_w, _F32),
-            d_logits=(d_logits, _F32), d_bias=(d_bias, _F32))
-    _need(bias, E, 4, "bias")
-    _need(mask, T, 1, "mask")
-    _need(counts, E, 4, "counts")
-    _need(n_live, 1, 4, "n_live")
-    _need(grad_loss, 1, 4, "grad_loss")
-    for t, name in ((topk_ids, "topk_ids"), (topk_w, "topk_w"), (d_topk_w, "d_topk_w")):
-        _need(t, T * k, 4, name)
-    _need(d_logits, T * E, 4, "d_logits")
-    _need(d_bias, E, 4, "d_bias")
-    p = _place(logits, bias, mask, counts, n_live, grad_loss, topk_ids, topk_w, d_topk_w, d_logits, d_bias, ws)
-    _check(_lib.coli_moe_balance_backward(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], T, E, k, p[9], p[10],
-                                          p[11], ws.numel() * ws.element_size(), _stream(stream)),
-           "coli_moe_balance_backward")
+    k = _rows(given, "topk_ids")[1]
+    p = _args(("logits", logits, _F32, None, False), ("bias", bias, _F32, E, False), ("mask", mask, _U8, T, False),
+              ("counts", counts, _I32, E, False), ("n_live", n_live, _I32, 1, False),
+              ("grad_loss", grad_loss, _F32, 1, False), ("topk_ids", topk_ids, _I32, T * k, False),
+              ("topk_w", topk_w, _F32, T * k, False), ("d_topk_w", d_topk_w, _F32, T * k, False),
+              ("d_logits", d_logits, _F32, T * E, False), ("d_bias", d_bias, _F32, E, False),
+              ("ws", ws, _ANY, None, False))
+    st = _lib.coli_moe_balance_backward(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], T, E, k, p[9], p[10], p[11],
+                                        ws.nbytes, _raw_stream(stream))
+    if st:
+        _check(st, "coli_moe_balance_backward")
 
 
 def coli_add_rmsnorm_fp8(x, residual, weight, eps: float, sum_out, norm_out, q, q_scale, stream=None):
     """Residual addition, root-mean-square norm and e4m3 rows with a scale per
     128 columns (see the header)."""
-    T, H = _rows(x, 2, "x")
-    _dtypes(x=(x, _BF16), residual=(residual, _BF16), weight=(weight, _BF16), sum_out=(sum_out, _BF16),
-            norm_out=(norm_out, _BF16), q=(q, _E4M3), q_scale=(q_scale, _F32))
-    _need(residual, T * H, 2, "residual")
-    _need(weight, H, 2, "weight")
-    _need(sum_out, T * H, 2, "sum_out")
-    _need(norm_out, T * H, 2, "norm_out")
-    _need(q, T * H, 1, "q")
-    _need(q_scale, T * (H // 128), 4, "q_scale")
-    p = _place(x, residual, weight, sum_out, norm_out, q, q_scale)
-    _check(_lib.coli_add_rmsnorm_fp8(p[0], p[1], p[2], eps, T, H, p[3], p[4], p[5], p[6], _stream(stream)),
-           "coli_add_rmsnorm_fp8")
+    T, H = _rows(x, "x")
+    n = T * H
+    p = _args(("x", x, _BF16, None, False), ("residual", residual, _BF16, n, False), ("weight", weight, _BF16, H, False),
+              ("sum_out", sum_out, _BF16, n, False), ("norm_out", norm_out, _BF16, n, False), ("q", q, _E4M3, n, False),
+              ("q_scale", q_scale, _F32, T * (H // 128), False))
+    st = _lib.coli_add_rmsnorm_fp8(p[0], p[1], p[2], eps, T, H, p[3], p[4], p[5], p[6], _raw_stream(stream))
+    if st:
+        _check(st, "coli_add_rmsnorm_fp8")
 
 
 def coli_fp8_matmul(a, a_scale, w, w_scale, out, stream=None):
     """out = (a * a_scale) @ (w * w_scale).T for e4m3 codes with a scale per row
     and 128 columns (a) and per 128 x 128 block (w); out: bf16 (2-byte elements)
     or fp32 [M, N] (see the header)."""
-    M, K = _rows(a, 1, "a")
-    N = _rows(w, 1, "w")[0]
+    M, K = _rows(a, "a")
+    N = _rows(w, "w")[0]
     nk = -(-K // 128)
-    f32 = out.element_size() == 4
-    _dtypes(a=(a, _E4M3), a_scale=(a_scale, _F32), w=(w, _E4M3), w_scale=(w_scale, _F32),
-            out=(out, _F32 if f32 else _BF16))
-    _need(w, N * K, 1, "w")
-    _need(a_scale, M * nk, 4, "a_scale")
-    _need(w_scale, -(-N // 128) * nk, 4, "w_scale")
-    _need(out, M * N, 4 if f32 else 2, "out")
-    p = _place(a, a_scale, w, w_scale, out)
-    _check(_lib.coli_fp8_matmul(p[0], p[1], p[2], p[3], M, N, K, p[4], COLI_FP8_OUT_F32 if f32 else 0, _stream(stream)),
-           "coli_fp8_matmul")
+    f32 = out.dtype == torch.float32
+    p = _args(("a", a, _E4M3, None, False), ("a_scale", a_scale, _F32, M * nk, False), ("w", w, _E4M3, N * K, False),
+              ("w_scale", w_scale, _F32, -(-N // 128) * nk, False), ("out", out, _F32 if f32 else _BF16, M * N, False))
+    st = _lib.coli_fp8_matmul(p[0], p[1], p[2], p[3], M, N, K, p[4], COLI_FP8_OUT_F32 if f32 else 0, _raw_stream(stream))
+    if st:
+        _check(st, "coli_fp8_matmul")
 
 
 def coli_moe_fp8_workspace_bytes(dims: coli_moe_dims, t_max: int) -> int:
@@ -494,25 +494,18 @@ def coli_moe_expert_ffn_fp8(dims, weights, x, x_scale, topk_ids, topk_w, unique_
                             residual, out, ws, stream=None):
     """Expert FFN + combine over e4m3 experts for a routed and unioned batch (see
     the header); weights: ``fp8_weights(...)``."""
-    T, H = _rows(x, 1, "x")
+    T, H = _rows(x, "x")
     if H != dims.hidden:
         raise ValueError(f"x: shape {tuple(x.shape)}, the call needs [T, {dims.hidden}]")
     P = T * dims.top_k
     U = min(dims.n_experts, P)
-    _dtypes(x=(x, _E4M3), x_scale=(x_scale, _F32), topk_ids=(topk_ids, _I32), topk_w=(topk_w, _F32),
-            unique_ids=(unique_ids, _I32), n_unique=(n_unique, _I32), seg_off=(seg_off, _I32), perm=(perm, _I32),
-            pair_pos=(pair_pos, _I32), residual=(residual, _BF16), out=(out, _BF16))
-    _need(x_scale, T * (H // 128), 4, "x_scale")
-    _need(topk_ids, P, 4, "topk_ids")
-    _need(topk_w, P, 4, "topk_w")
-    _need(unique_ids, U, 4, "unique_ids", at_least=True)
-    _need(n_unique, 1, 4, "n_unique", at_least=True)
-    _need(seg_off, U + 1, 4, "seg_off", at_least=True)
-    _need(perm, P, 4, "perm", at_least=True)
-    _need(pair_pos, P, 4, "pair_pos", at_least=True)
-    _need(residual, T * H, 2, "residual")
-    _need(out, T * H, 2, "out")
-    p = _place(x, x_scale, topk_ids, topk_w, unique_ids, n_unique, seg_off, perm, pair_pos, residual, out, ws)
-    _check(_lib.coli_moe_expert_ffn_fp8(ctypes.byref(dims), ctypes.byref(weights), p[0], p[1], T, p[2], p[3], p[4],
-                                        p[5], p[6], p[7], p[8], p[9], p[10], p[11], ws.numel() * ws.element_size(),
-                                        _stream(stream)), "coli_moe_expert_ffn_fp8")
+    p = _args(("x", x, _E4M3, None, False), ("x_scale", x_scale, _F32, T * (H // 128), False),
+              ("topk_ids", topk_ids, _I32, P, False), ("topk_w", topk_w, _F32, P, False),
+              ("unique_ids", unique_ids, _I32, U, True), ("n_unique", n_unique, _I32, 1, True),
+              ("seg_off", seg_off, _I32, U + 1, True), ("perm", perm, _I32, P, True),
+              ("pair_pos", pair_pos, _I32, P, True), ("residual", residual, _BF16, T * H, False),
+              ("out", out, _BF16, T * H, False), ("ws", ws, _ANY, None, False))
+    st = _lib.coli_moe_expert_ffn_fp8(ctypes.byref(dims), ctypes.byref(weights), p[0], p[1], T, p[2], p[3], p[4], p[5],
+                                      p[6], p[7], p[8], p[9], p[10], p[11], ws.nbytes, _raw_stream(stream))
+    if st:
+        _check(st, "coli_moe_expert_ffn_fp8")

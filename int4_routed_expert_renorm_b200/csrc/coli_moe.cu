@@ -112,6 +112,22 @@ bool fp8_kernels_ready() {
          fp8_kernel_ready<1, kF8Tokens, false>();
 }
 
+// The balance kernels keep up to 17 rows of 1024 floats in shared memory.
+template <int NV, int VEC>
+bool balance_kernel_ready() {
+  const int smem = (kBalWarps + 1) * 32 * NV * 4;
+  return cudaFuncSetAttribute(balance_kernel<NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+             cudaSuccess &&
+         cudaFuncSetAttribute(balance_backward_kernel<NV, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+             cudaSuccess;
+}
+
+bool balance_kernels_ready() {
+  return balance_kernel_ready<4, 4>() && balance_kernel_ready<4, 1>() && balance_kernel_ready<8, 4>() &&
+         balance_kernel_ready<8, 1>() && balance_kernel_ready<16, 4>() && balance_kernel_ready<16, 1>() &&
+         balance_kernel_ready<32, 4>() && balance_kernel_ready<32, 1>();
+}
+
 struct DevInfo {
   uint32_t* status;
   int sms;
@@ -165,7 +181,7 @@ coli_status dev_info(DevInfo* out) {
     COLI_SET_SK_SMEM(1, 64, 8)
     COLI_SET_SK_SMEM(2, 64, 8)
 #undef COLI_SET_SK_SMEM
-    ok &= fp8_kernels_ready();
+    ok &= fp8_kernels_ready() && balance_kernels_ready();
     ok &= cudaFuncSetAttribute(logits_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
           cudaSuccess;
     ok &= cudaFuncSetAttribute(union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

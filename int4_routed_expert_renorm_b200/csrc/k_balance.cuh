@@ -11,17 +11,40 @@
 // constant may be taken off every f_e; 1/E is, as (E c_e - n k) / (n k E) with an
 // exact integer numerator, so that nearly balanced experts do not cancel.
 //
-// One warp owns a token's row: E <= 1024 values in registers, read once.  The
-// kernels are bound by HBM (4 bytes per logit read forward; 4 read and 4
-// written backward) for large batches and by launch latency for small ones.
-// Column sums (P, the bias gradient) are summed per warp in registers, then over
-// a block's warps, then over the blocks, each in a fixed order: no float atomics.
+// One warp owns a token's row: E <= 1024 values in registers, read once, the next
+// token's row on its way.  Column sums (P, the bias gradient) are summed per warp
+// in registers, then over a block's warps, then over the blocks, each in a fixed
+// order: no float atomics.  Up to kBalFused tokens one cluster of 8 blocks does
+// everything in one launch, adding over the blocks through distributed shared
+// memory; larger batches write their blocks' sums to the workspace and a second
+// launch adds them.
+// Bound by HBM (4 bytes per logit read forward; 4 read and 4 written backward) for
+// large batches and by latency for small ones.
 #pragma once
 #include "common.cuh"
 
 namespace coli {
 
-constexpr int kBalWarps = 8;
+constexpr int kBalWarps = 16;          // per block
+constexpr int kBalCluster = 8;
+constexpr int kBalFused = 256;         // tokens: two rows per warp of the cluster
+constexpr int kBalMaxBlocks = 296;     // two per SM
+
+__device__ __forceinline__ void bal_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t bal_cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The 32 bits at this block's shared address p in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t bal_peer(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
 
 // Warp-wide sum and maximum, the same value in every lane.
 __device__ __forceinline__ float warp_sum(float v) {
@@ -30,9 +53,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  // as integers of the same order: one instruction over the warp
+  const uint32_t u = __float_as_uint(v);
+  const uint32_t m = __reduce_max_sync(0xffffffffu, (u & 0x80000000u) ? ~u : (u | 0x80000000u));
+  return __uint_as_float((m & 0x80000000u) ? (m & 0x7fffffffu) : ~m);
 }
 
 // Lane `lane` holds experts e(q) = (q / VEC * 32 + lane) * VEC + q % VEC of a row.
@@ -91,10 +115,10 @@ __device__ __forceinline__ bool bal_softmax(float (&v)[NV], const float (&b)[NV]
   return bad;
 }
 
-// Adds the kBalWarps warps' column sums in warp order and writes the block's
-// row of `part` ([blocks][E]).  `sm` holds E floats per warp.
-template <int NV, int VEC>
-__device__ __forceinline__ void bal_block_columns(const float (&acc)[NV], int E, float* sm, float* __restrict__ part) {
+// Adds the kBalWarps warps' column sums in warp order: thread e gets columns e,
+// e + blockDim.x ..  `sm` holds E floats per warp; fn(e, sum) takes each.
+template <int NV, int VEC, typename F>
+__device__ __forceinline__ void bal_block_columns(const float (&acc)[NV], int E, float* sm, F fn) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int q = 0; q < NV; ++q) {
@@ -106,28 +130,76 @@ __device__ __forceinline__ void bal_block_columns(const float (&acc)[NV], int E,
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kBalWarps; ++w) s += sm[w * E + e];
-    part[static_cast<size_t>(blockIdx.x) * E + e] = s;
+    fn(e, s);
   }
 }
 
-// Forward, first pass: each block's sums of p, pair counts and live tokens.
-// Dynamic shared memory: (kBalWarps + 1) * E words.
+// What is left of one expert once its column sum p and count c are known; its term of the loss.
+__device__ __forceinline__ double bal_expert_out(float p, int c, int n, int k, int32_t* counts, float* prob_mean) {
+  const float mean = n > 0 ? p / static_cast<float>(n) : 0.f;
+  *counts = c;
+  *prob_mean = mean;
+  return n > 0 ? static_cast<double>(c) * mean / (static_cast<double>(n) * k) : 0.0;
+}
+
+// Sum of v over a block of NT threads in a fixed order (valid in thread 0); `sm`: NT / 32 doubles.
+template <int NT>
+__device__ __forceinline__ double bal_block_sum(double v, double* sm) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < NT / 32; ++w) s += sm[w];
+  return s;
+}
+
+// Adds the cluster's loss terms in rank order and writes the loss.  Ends with a
+// cluster barrier: the peers' shared memory is read before it.
+__device__ __forceinline__ void bal_cluster_loss(double mine, double* slot, int E, int n, float* loss, int32_t* n_live) {
+  if (threadIdx.x == 0) *slot = mine;
+  bal_cluster_sync();
+  if (bal_cluster_rank() == 0 && threadIdx.x == 0) {
+    double s = 0.0;
+    for (int r = 0; r < kBalCluster; ++r) {
+      const uint32_t* p = reinterpret_cast<const uint32_t*>(slot);
+      s += __hiloint2double(static_cast<int>(bal_peer(p + 1, r)), static_cast<int>(bal_peer(p, r)));
+    }
+    *loss = static_cast<float>(E * s);
+    *n_live = n;
+  }
+  bal_cluster_sync();
+}
+
+struct BalOut {
+  int32_t* counts;
+  int32_t* n_live;
+  float* prob_mean;
+  float* loss;
+};
+
+// Forward: each block's sums of p, pair counts and live tokens.  With `fused` the
+// grid is one cluster, which goes on to the results; otherwise they are left in
+// part_*.  Dynamic shared memory: (kBalWarps + 1) * E words.
 template <int NV, int VEC>
 __global__ void __launch_bounds__(kBalWarps * 32)
-    balance_partial_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
-                           const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T, int E, int k,
-                           float* __restrict__ part_p, int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
-                           uint32_t* __restrict__ status) {
+    balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias, const int32_t* __restrict__ ids,
+                   const uint8_t* __restrict__ mask, int T, int E, int k, int fused, float* __restrict__ part_p,
+                   int32_t* __restrict__ part_c, int32_t* __restrict__ part_n, BalOut out,
+                   uint32_t* __restrict__ status) {
   extern __shared__ float bal_sm[];
   int32_t* hist = reinterpret_cast<int32_t*>(bal_sm + kBalWarps * E);
   __shared__ int live_n;
+  __shared__ double loss_sm[kBalWarps + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
   if (threadIdx.x == 0) live_n = 0;
   pdl_wait();
   pdl_trigger();
   __syncthreads();
-  float b[NV], acc[NV];
+  constexpr bool AHEAD = NV < 32;      // registers for the next row
+  float b[NV], acc[NV], v[NV], nx[AHEAD ? NV : 1];
 #pragma unroll
   for (int q = 0; q < NV; ++q) {
     b[q] = 0.f;
@@ -135,13 +207,30 @@ __global__ void __launch_bounds__(kBalWarps * 32)
   }
   if (bias) bal_load<NV, VEC>(bias, E, lane, 0.f, b);
   uint32_t flags = 0;
-  int live = 0;
-  for (int t = blockIdx.x * kBalWarps + warp; t < T; t += gridDim.x * kBalWarps) {
-    if (mask && mask[t] == 0) continue;
-    float v[NV];
-    bal_load<NV, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, v);
+  int live = 0, id = 0, idn = 0;
+  bool on = false, onn = false;
+  const int step = gridDim.x * kBalWarps;
+  auto fetch = [&](int t) {
+    onn = t < T && (!mask || mask[t] != 0);
+    if (onn) {
+      if constexpr (AHEAD) bal_load<NV, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, nx);
+      if (lane < k) idn = __ldg(ids + static_cast<size_t>(t) * k + lane);
+    }
+  };
+  const int t0 = blockIdx.x * kBalWarps + warp;
+  fetch(t0);
+  for (int t = t0; t < T; t += step) {
+    on = onn;
+    id = idn;
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int q = 0; q < NV; ++q) v[q] = nx[q];
+    } else if (on) {
+      bal_load<NV, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, v);
+    }
+    fetch(t + step);
+    if (!on) continue;
     if (lane < k) {
-      const int id = __ldg(ids + static_cast<size_t>(t) * k + lane);
       if (id >= 0 && id < E)
         atomicAdd(hist + id, 1);
       else
@@ -154,74 +243,113 @@ __global__ void __launch_bounds__(kBalWarps * 32)
   }
   if (lane == 0 && live) atomicAdd(&live_n, live);
   if (flags) atomicOr(status, flags);
-  bal_block_columns<NV, VEC>(acc, E, bal_sm, part_p);   // its barrier also covers hist and live_n
-  for (int e = threadIdx.x; e < E; e += blockDim.x) part_c[static_cast<size_t>(blockIdx.x) * E + e] = hist[e];
-  if (threadIdx.x == 0) part_n[blockIdx.x] = live_n;
+  if (!fused) {
+    // the barrier inside also covers hist and live_n
+    bal_block_columns<NV, VEC>(acc, E, bal_sm, [&](int e, float s) {
+      part_p[static_cast<size_t>(blockIdx.x) * E + e] = s;
+      part_c[static_cast<size_t>(blockIdx.x) * E + e] = hist[e];
+    });
+    if (threadIdx.x == 0) part_n[blockIdx.x] = live_n;
+    return;
+  }
+  // block sums over warp 0's row (each thread reads and writes its own columns)
+  bal_block_columns<NV, VEC>(acc, E, bal_sm, [&](int e, float s) { bal_sm[e] = s; });
+  bal_cluster_sync();
+  const uint32_t rank = bal_cluster_rank();
+  int n = 0;
+  for (int r = 0; r < kBalCluster; ++r) n += static_cast<int>(bal_peer(&live_n, r));
+  double term = 0.0;
+  for (int e = rank + kBalCluster * threadIdx.x; e < E; e += kBalCluster * blockDim.x) {
+    float p = 0.f;
+    int c = 0;
+    for (int r = 0; r < kBalCluster; ++r) {
+      p += __uint_as_float(bal_peer(bal_sm + e, r));
+      c += static_cast<int>(bal_peer(hist + e, r));
+    }
+    term += bal_expert_out(p, c, n, k, out.counts + e, out.prob_mean + e);
+  }
+  term = bal_block_sum<kBalWarps * 32>(term, loss_sm);
+  bal_cluster_loss(term, loss_sm + kBalWarps, E, n, out.loss, out.n_live);
 }
 
-// Forward, second pass (one block of 1024 threads): the blocks' rows added in
-// block order; counts, mean probabilities, live tokens and the loss.
-__global__ void __launch_bounds__(1024)
+constexpr int kBalGroup = 16;          // warps that share a column's rows in the second passes
+
+// Second pass of the forward (one cluster): the blocks' rows added in a fixed
+// order, then the results.
+__global__ void __launch_bounds__(512)
     balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
-                          const int32_t* __restrict__ part_n, int blocks, int E, int k, int32_t* __restrict__ counts,
-                          int32_t* __restrict__ n_live, float* __restrict__ prob_mean, float* __restrict__ loss) {
-  __shared__ double sm[32];
+                          const int32_t* __restrict__ part_n, int blocks, int E, int k, BalOut out) {
+  __shared__ float ps[kBalGroup][33];
+  __shared__ int cs[kBalGroup][33];
+  __shared__ double loss_sm[17];
   __shared__ int n_sm;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < 32) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
     int n = 0;
-    for (int i = threadIdx.x; i < blocks; i += 32) n += part_n[i];
+    for (int i = lane; i < blocks; i += 32) n += part_n[i];
     n = __reduce_add_sync(0xffffffffu, n);
-    if (threadIdx.x == 0) n_sm = n;
+    if (lane == 0) n_sm = n;
+  }
+  double term = 0.0;
+  // 32 neighbouring columns at a time (rows of 128 bytes), a warp per row group
+  for (int e0 = 32 * static_cast<int>(bal_cluster_rank()); e0 < E; e0 += 32 * kBalCluster) {
+    const int e = e0 + lane;
+    float p = 0.f;
+    int c = 0;
+    if (e < E) {
+#pragma unroll 4
+      for (int i = warp; i < blocks; i += kBalGroup) {
+        p += part_p[static_cast<size_t>(i) * E + e];
+        c += part_c[static_cast<size_t>(i) * E + e];
+      }
+    }
+    ps[warp][lane] = p;
+    cs[warp][lane] = c;
+    __syncthreads();
+    if (warp == 0 && e < E) {
+      p = 0.f;
+      c = 0;
+#pragma unroll
+      for (int w = 0; w < kBalGroup; ++w) {
+        p += ps[w][lane];
+        c += cs[w][lane];
+      }
+      term += bal_expert_out(p, c, n_sm, k, out.counts + e, out.prob_mean + e);
+    }
+    __syncthreads();
   }
   __syncthreads();
   const int n = n_sm;
-  const int e = threadIdx.x;
-  double term = 0.0;
-  if (e < E) {
-    float p = 0.f;
-    int c = 0;
-    for (int i = 0; i < blocks; ++i) {
-      p += part_p[static_cast<size_t>(i) * E + e];
-      c += part_c[static_cast<size_t>(i) * E + e];
-    }
-    const float mean = n > 0 ? p / static_cast<float>(n) : 0.f;
-    counts[e] = c;
-    prob_mean[e] = mean;
-    term = n > 0 ? static_cast<double>(c) * mean / (static_cast<double>(n) * k) : 0.0;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = term;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int w = 0; w < 32; ++w) s += sm[w];
-    *loss = static_cast<float>(E * s);
-    *n_live = n;
-  }
+  term = bal_block_sum<512>(term, loss_sm);
+  bal_cluster_loss(term, loss_sm + 16, E, n, out.loss, out.n_live);
 }
 
-// Backward: d_logits, and each block's column sums when part_b is not NULL.
-// Dynamic shared memory: kBalWarps * E floats when part_b is not NULL.
+// Backward: d_logits, and the column sums when d_bias is not NULL: with `fused`
+// (one cluster) added over the blocks here, otherwise left in part_b.  Dynamic
+// shared memory: kBalWarps * E floats (a row of the selected experts' terms per
+// warp, then the column sums).
 template <int NV, int VEC>
 __global__ void __launch_bounds__(kBalWarps * 32)
-    balance_backward_kernel(const float* logits, const float* __restrict__ bias,
-                            const uint8_t* __restrict__ mask, const int32_t* __restrict__ counts,
-                            const int32_t* __restrict__ n_live, const float* __restrict__ grad_loss,
-                            const int32_t* __restrict__ ids, const float* __restrict__ w,
-                            const float* __restrict__ d_w, int T, int E, int k, float* d_logits,
-                            float* __restrict__ part_b) {
+    balance_backward_kernel(const float* logits, const float* __restrict__ bias, const uint8_t* __restrict__ mask,
+                            const int32_t* __restrict__ counts, const int32_t* __restrict__ n_live,
+                            const float* __restrict__ grad_loss, const int32_t* __restrict__ ids,
+                            const float* __restrict__ w, const float* __restrict__ d_w, int T, int E, int k, int fused,
+                            float* d_logits, float* __restrict__ part_b, float* __restrict__ d_bias) {
   extern __shared__ float bal_sm[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* sel = bal_sm + warp * E;      // zero between tokens
+  for (int e = lane; e < E; e += 32) sel[e] = 0.f;
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncwarp();
   const int n = __ldg(n_live);
   const long long nk = static_cast<long long>(n) * k;
   const float coef = grad_loss && n > 0 ? __ldg(grad_loss) * static_cast<float>(E) / static_cast<float>(n) : 0.f;
   const float fscale = n > 0 ? static_cast<float>(1.0 / (static_cast<double>(nk) * E)) : 0.f;
-  float b[NV], f[NV], acc[NV];
+  constexpr bool AHEAD = NV < 32;      // registers for the next row
+  float b[NV], f[NV], acc[NV], v[NV], nx[AHEAD ? NV : 1];
 #pragma unroll
   for (int q = 0; q < NV; ++q) {
     const int e = bal_expert<VEC>(q, lane);
@@ -230,42 +358,85 @@ __global__ void __launch_bounds__(kBalWarps * 32)
     f[q] = e < E ? static_cast<float>(static_cast<long long>(E) * __ldg(counts + e) - nk) * fscale : 0.f;
   }
   if (bias) bal_load<NV, VEC>(bias, E, lane, 0.f, b);
-  for (int t = blockIdx.x * kBalWarps + warp; t < T; t += gridDim.x * kBalWarps) {
-    float v[NV];
-    if (mask && mask[t] == 0) {
+  bool on = false, onn = false;
+  int id = -1, idn = -1;
+  float wj = 0.f, dj = 0.f, wn = 0.f, dn = 0.f;
+  const int step = gridDim.x * kBalWarps;
+  auto fetch = [&](int t) {
+    onn = t < T && (!mask || mask[t] != 0);
+    if (!onn) return;
+    if constexpr (AHEAD) {
+      if (coef != 0.f) bal_load<NV, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, nx);
+    }
+    if (d_w && lane < k) {
+      const size_t at = static_cast<size_t>(t) * k + lane;
+      idn = __ldg(ids + at);
+      wn = __ldg(w + at);
+      dn = __ldg(d_w + at);
+    }
+  };
+  const int t0 = blockIdx.x * kBalWarps + warp;
+  fetch(t0);
+  for (int t = t0; t < T; t += step) {
+    on = onn;
+    id = idn;
+    wj = wn;
+    dj = dn;
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int q = 0; q < NV; ++q) v[q] = nx[q];
+    } else if (on && coef != 0.f) {
+      bal_load<NV, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, v);
+    }
+    fetch(t + step);
+    if (on && coef != 0.f) {
+      bal_softmax<NV>(v, b);
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < NV; ++q) s = fmaf(v[q], f[q], s);
+      s = warp_sum(s);
+#pragma unroll
+      for (int q = 0; q < NV; ++q) v[q] = coef * v[q] * (f[q] - s);
+    } else {
 #pragma unroll
       for (int q = 0; q < NV; ++q) v[q] = 0.f;
-    } else {
-      if (coef != 0.f) {
-        bal_load<NV, VEC>(logits + static_cast<size_t>(t) * E, E, lane, -INFINITY, v);
-        bal_softmax<NV>(v, b);
-        float s = 0.f;
-#pragma unroll
-        for (int q = 0; q < NV; ++q) s = fmaf(v[q], f[q], s);
-        s = warp_sum(s);
-#pragma unroll
-        for (int q = 0; q < NV; ++q) v[q] = coef * v[q] * (f[q] - s);
-      } else {
-#pragma unroll
-        for (int q = 0; q < NV; ++q) v[q] = 0.f;
-      }
-      if (d_w) {
-        const size_t at = static_cast<size_t>(t) * k + lane;
-        const int id = lane < k ? __ldg(ids + at) : -1;
-        const float wj = lane < k ? __ldg(w + at) : 0.f;
-        const float dj = lane < k ? __ldg(d_w + at) : 0.f;
-        const float sj = wj * (dj - warp_sum(wj * dj));
+    }
+    if (on && d_w) {
+      const float sj = wj * (dj - warp_sum(wj * dj));
+      const bool mine = lane < k && static_cast<unsigned>(id) < static_cast<unsigned>(E);
+      // the selected experts' terms through a row of shared memory; the same
+      // expert twice is added in slot order
+      const unsigned same = __match_any_sync(0xffffffffu, mine ? id : -1 - lane);
+      if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
         for (int j = 0; j < k; ++j) {
-          const int ej = __shfl_sync(0xffffffffu, id, j);
-          const float gj = __shfl_sync(0xffffffffu, sj, j);
+          if (lane == j && mine) sel[id] += sj;
+          __syncwarp();
+        }
+      } else if (mine) {
+        sel[id] = sj;
+      }
+      __syncwarp();
 #pragma unroll
-          for (int q = 0; q < NV; ++q)
-            if (bal_expert<VEC>(q, lane) == ej) v[q] += gj;
+      for (int q = 0; q < NV; q += VEC) {
+        const int e = bal_expert<VEC>(q, lane);
+        if (e < E) {
+          if (VEC == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sel + e);
+            v[q] += x.x;
+            v[q + 1 < NV ? q + 1 : q] += x.y;
+            v[q + 2 < NV ? q + 2 : q] += x.z;
+            v[q + 3 < NV ? q + 3 : q] += x.w;
+          } else {
+            v[q] += sel[e];
+          }
         }
       }
-#pragma unroll
-      for (int q = 0; q < NV; ++q) acc[q] += v[q];
+      __syncwarp();
+      if (mine) sel[id] = 0.f;
+      __syncwarp();
     }
+#pragma unroll
+    for (int q = 0; q < NV; ++q) acc[q] += v[q];
     float* row = d_logits + static_cast<size_t>(t) * E;
 #pragma unroll
     for (int q = 0; q < NV; q += VEC) {
@@ -279,19 +450,43 @@ __global__ void __launch_bounds__(kBalWarps * 32)
       }
     }
   }
-  if (part_b) bal_block_columns<NV, VEC>(acc, E, bal_sm, part_b);
+  if (!d_bias) return;
+  if (!fused) {
+    bal_block_columns<NV, VEC>(acc, E, bal_sm,
+                               [&](int e, float s) { part_b[static_cast<size_t>(blockIdx.x) * E + e] = s; });
+    return;
+  }
+  bal_block_columns<NV, VEC>(acc, E, bal_sm, [&](int e, float s) { bal_sm[e] = s; });
+  bal_cluster_sync();
+  for (int e = bal_cluster_rank() + kBalCluster * threadIdx.x; e < E; e += kBalCluster * blockDim.x) {
+    float s = 0.f;
+    for (int r = 0; r < kBalCluster; ++r) s += __uint_as_float(bal_peer(bal_sm + e, r));
+    d_bias[e] = s;
+  }
+  bal_cluster_sync();
 }
 
-// d_bias[e] = the blocks' column sums added in block order.
-__global__ void __launch_bounds__(256) balance_bias_kernel(const float* __restrict__ part_b, int blocks, int E,
+// d_bias: the blocks' column sums added in a fixed order, 32 columns a block.
+__global__ void __launch_bounds__(512) balance_bias_kernel(const float* __restrict__ part_b, int blocks, int E,
                                                            float* __restrict__ d_bias) {
+  __shared__ float ps[kBalGroup][33];
   pdl_wait();
   pdl_trigger();
-  const int e = blockIdx.x * blockDim.x + threadIdx.x;
-  if (e >= E) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int e = blockIdx.x * 32 + lane;
   float s = 0.f;
-  for (int i = 0; i < blocks; ++i) s += part_b[static_cast<size_t>(i) * E + e];
-  d_bias[e] = s;
+  if (e < E) {
+#pragma unroll 4
+    for (int i = warp; i < blocks; i += kBalGroup) s += part_b[static_cast<size_t>(i) * E + e];
+  }
+  ps[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && e < E) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBalGroup; ++w) s += ps[w][lane];
+    d_bias[e] = s;
+  }
 }
 
 }  // namespace coli

@@ -6,9 +6,33 @@ namespace {
 
 // ---- balance ---------------------------------------------------------------
 
-// Blocks of a balance pass: a token per warp, at most two blocks per SM of the
-// largest part (148 SMs), so that the workspace depends on T and E alone.
-inline int balance_blocks(int T) { return std::min((T + kBalWarps - 1) / kBalWarps, 296); }
+// Blocks of a balance pass: one cluster up to kBalFused tokens, else a token per
+// warp up to kBalMaxBlocks, so that the workspace depends on T and E alone.
+inline bool balance_fused(int T) { return T <= kBalFused; }
+inline int balance_blocks(int T) {
+  return balance_fused(T) ? kBalCluster : std::min((T + kBalWarps - 1) / kBalWarps, kBalMaxBlocks);
+}
+
+template <typename... KArgs, typename... Args>
+bool launch_balance(void (*kernel)(KArgs...), int grid, bool cluster, int threads, size_t smem, cudaStream_t st,
+                    Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kBalCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  ++t_launches;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess;
+}
 
 struct BalWs {
   float* p;      // [blocks][E] column sums
@@ -156,23 +180,22 @@ coli_status coli_moe_balance(const float* logits, const float* bias, const int32
   DevInfo di;
   if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
-  const int blocks = balance_blocks(T);   // 0 for an empty batch: counts, means and loss are zero
-  if (T > 0) {
-    const bool vec = balance_vec4(E, logits, bias, nullptr);
-    const size_t smem = static_cast<size_t>(kBalWarps + 1) * E * 4;
-    bool ok;
+  const int blocks = balance_blocks(T);
+  const bool fused = balance_fused(T);
+  const bool vec = balance_vec4(E, logits, bias, nullptr);
+  const size_t smem = static_cast<size_t>(kBalWarps + 1) * E * 4;
+  const BalOut out{counts, n_live, prob_mean, loss};
+  bool ok;
 #define COLI_BAL_FWD(NV, VEC)                                                                                     \
-  launch(balance_partial_kernel<NV, VEC>, dim3(blocks), dim3(kBalWarps * 32), smem, s, logits, bias, topk_ids, mask, \
-         T, E, k, w.p, w.c, w.n, di.status)
-    COLI_BAL_DISPATCH(E, vec, COLI_BAL_FWD)
+  launch_balance(balance_kernel<NV, VEC>, blocks, fused, kBalWarps * 32, smem, s, logits, bias, topk_ids, mask, T, E, \
+                 k, fused ? 1 : 0, w.p, w.c, w.n, out, di.status)
+  COLI_BAL_DISPATCH(E, vec, COLI_BAL_FWD)
 #undef COLI_BAL_FWD
-    if (!ok) return COLI_ERR_CUDA;
-  }
-  return launch(balance_finish_kernel, dim3(1), dim3(1024), 0, s, static_cast<const float*>(w.p),
-                static_cast<const int32_t*>(w.c), static_cast<const int32_t*>(w.n), blocks, E, k, counts, n_live,
-                prob_mean, loss)
-             ? COLI_OK
-             : COLI_ERR_CUDA;
+  if (!ok) return COLI_ERR_CUDA;
+  if (!fused && !launch_balance(balance_finish_kernel, kBalCluster, true, 512, 0, s, static_cast<const float*>(w.p),
+                                static_cast<const int32_t*>(w.c), static_cast<const int32_t*>(w.n), blocks, E, k, out))
+    return COLI_ERR_CUDA;
+  return COLI_OK;
 }
 
 coli_status coli_moe_balance_backward(const float* logits, const float* bias, const uint8_t* mask,
@@ -190,20 +213,18 @@ coli_status coli_moe_balance_backward(const float* logits, const float* bias, co
   if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
   const int blocks = balance_blocks(T);
-  if (T > 0) {
-    const bool vec = balance_vec4(E, logits, bias, d_logits);
-    const size_t smem = d_bias ? static_cast<size_t>(kBalWarps) * E * 4 : 0;
-    float* part = d_bias ? w.p : nullptr;
-    bool ok;
-#define COLI_BAL_BWD(NV, VEC)                                                                                  \
-  launch(balance_backward_kernel<NV, VEC>, dim3(blocks), dim3(kBalWarps * 32), smem, s, logits, bias, mask, counts, \
-         n_live, grad_loss, topk_ids, topk_w, d_topk_w, T, E, k, d_logits, part)
-    COLI_BAL_DISPATCH(E, vec, COLI_BAL_BWD)
+  const bool fused = balance_fused(T);
+  const bool vec = balance_vec4(E, logits, bias, d_logits);
+  const size_t smem = static_cast<size_t>(kBalWarps) * E * 4;
+  bool ok;
+#define COLI_BAL_BWD(NV, VEC)                                                                                    \
+  launch_balance(balance_backward_kernel<NV, VEC>, blocks, fused, kBalWarps * 32, smem, s, logits, bias, mask, counts, \
+                 n_live, grad_loss, topk_ids, topk_w, d_topk_w, T, E, k, fused ? 1 : 0, d_logits, w.p, d_bias)
+  COLI_BAL_DISPATCH(E, vec, COLI_BAL_BWD)
 #undef COLI_BAL_BWD
-    if (!ok) return COLI_ERR_CUDA;
-  }
-  if (d_bias && !launch(balance_bias_kernel, dim3((E + 255) / 256), dim3(256), 0, s, static_cast<const float*>(w.p),
-                        blocks, E, d_bias))
+  if (!ok) return COLI_ERR_CUDA;
+  if (d_bias && !fused && !launch(balance_bias_kernel, dim3((E + 31) / 32), dim3(512), 0, s,
+                                  static_cast<const float*>(w.p), blocks, E, d_bias))
     return COLI_ERR_CUDA;
   return COLI_OK;
 }
