@@ -73,12 +73,13 @@ struct F8Cfg {
   static constexpr int SLOT = 128;
   static constexpr int NSLOT = 4;
   static constexpr int META_INTS = 2 * kF8MaxSeg + 4 + kF8MaxSeg / 2;
-  static constexpr int FIXED = 4 * 128 * 4 + META_INTS * 4 + 512;
+  static constexpr int SCG = 4 * NMAT * 128;                        // scales of a group of four K blocks
+  static constexpr int FIXED = 2 * SCG * 4 + 4 * 128 * 4 + META_INTS * 4 + 512;
   static constexpr int NST = (232448 - 1024 - FIXED) / (WSTAGE + ASTAGE);
   static constexpr size_t SMEM = 1024 + static_cast<size_t>(NST) * (WSTAGE + ASTAGE) + FIXED;
   static constexpr int TOT_LD = NT + 1;                             // split K: totals [column][TOT_LD]
   static_assert(NT % 32 == 0 && NT <= 128, "a tile's tokens are tensor-memory lanes");
-  static_assert(NST >= 3 && 2 * NST + NSLOT + 5 <= 60 && NST > NSLOT / NMAT, "stages");
+  static_assert(NST >= 3 && 2 * NST + NSLOT + 9 <= 60 && NST > NSLOT / NMAT, "stages");
   // the A operand's descriptor spans 128 rows whatever NT: the weight stages that
   // follow the token stages keep that inside the allocation
   static_assert(NST * WSTAGE >= 128 * 128 && ASTAGE % 1024 == 0, "operand extent");
@@ -172,6 +173,10 @@ __device__ __forceinline__ float ldg_here(const float* p) {
   float v;
   asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
+}
+
+__device__ __forceinline__ void ldg4_here(const float* p, float (&v)[4]) {
+  asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p));
 }
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
@@ -338,7 +343,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint8_t* a_stages = smem;                                              // token rows
   uint8_t* w_stages = smem + C::NST * C::ASTAGE;                         // weight rows
   float* red = reinterpret_cast<float*>(w_stages + C::NST * C::WSTAGE);  // [2 parities][2 halves][128]: maxima
-  int32_t* blk_off = reinterpret_cast<int32_t*>(red + 4 * 128);
+  float* scales = red + 4 * 128;                                         // [2][4][NMAT][128]
+  int32_t* blk_off = reinterpret_cast<int32_t*>(scales + 2 * C::SCG);
   int32_t* seg = blk_off + kF8MaxSeg + 2;
   uint16_t* uniq = reinterpret_cast<uint16_t*>(seg + kF8MaxSeg + 2);      // expert ids below 1024
   uint64_t* bars = reinterpret_cast<uint64_t*>(blk_off + C::META_INTS);
@@ -346,7 +352,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint64_t* done = full + C::NST;                 // the stage's MMAs are complete
   uint64_t* slot_empty = done + C::NST;
   uint64_t* pair_bar = slot_empty + C::NSLOT;      // [4]: the two warps of a lane quarter
-  uint64_t* mma_done = pair_bar + 4;
+  uint64_t* sc_full = pair_bar + 4;                // [2]: a group's scales are written
+  uint64_t* sc_empty = sc_full + 2;                // and read
+  uint64_t* mma_done = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* scratch = reinterpret_cast<int*>(red);     // 33 ints, before the tiles
@@ -361,6 +369,10 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(&slot_empty[q], 8);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 2);
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&sc_full[q], 2);
+      mbar_init(&sc_empty[q], 8);
+    }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -508,6 +520,72 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         mbar_wait(mma_done, 0, reinterpret_cast<volatile int*>(&dummy), a.status);
       }
       __syncwarp();
+    } else {
+      // ----------------------------------------------------------- scales
+      // Warps 2 and 3: the tile's scales, token's times weight block's, four K
+      // blocks at a time, to shared memory.  A warp's 32 rows are 32 lines, and a
+      // line costs the shared-memory pipe as much as 128 bytes of operands: they
+      // are read once here (16 bytes a line where rows allow it) rather than by the
+      // totals' eight warps.  Warp 2 + w takes tokens 32 w .. and 64 + 32 w ..; the
+      // next four K blocks are on their way.
+      constexpr int NI = NT > 64 ? 2 : 1;
+      const int c0 = lane + 32 * (warp - 2);
+      const bool rows4 = a.nk % 4 == 0 && kb0 % 4 == 0 && kb1 % 4 == 0 && (reinterpret_cast<uintptr_t>(a.a_s) & 15) == 0;
+      const float* ap[NI];
+      const float* wp[NMAT];
+      float an[NI][4], wn[NMAT][4];
+      auto set_tile = [&](int t) {
+        const F8Tile ti = tile_at(t);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) ap[i] = a.a_s + static_cast<size_t>(f8_row(a, ti, c0 + 64 * i)) * a.nk;
+#pragma unroll
+        for (int m = 0; m < NMAT; ++m) {
+          const int rb = GU ? ti.rblk : min(ti.rblk * NMAT + m, nrb - 1);
+          wp[m] = (GU && m ? a.w_s1 : a.w_s) + (static_cast<size_t>(ti.e) * nrb + rb) * a.nk;
+        }
+      };
+      auto load = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          if (rows4) {
+            ldg4_here(ap[i] + g, an[i]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) an[i][c] = ldg_here(ap[i] + min(g + c, kb1 - 1));
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) wn[m][c] = ldg_here(wp[m] + min(g + c, kb1 - 1));
+      };
+      bool ok = true;
+      uint32_t gi = 0;
+      if (t_first < tiles) {
+        set_tile(t_first);
+        load(kb0);
+      }
+      for (int t = t_first; ok && t < tiles; t += t_step) {
+        for (int g = kb0; g < kb1; g += 4, ++gi) {
+          if (!(ok = warp_wait(&sc_empty[gi & 1u], ((gi >> 1) & 1u) ^ 1u, abort_flag, a.status))) break;
+          float* to = scales + (gi & 1u) * C::SCG;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+              for (int i = 0; i < NI; ++i) to[(c * NMAT + m) * 128 + c0 + 64 * i] = an[i][c] * wn[m][c];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[gi & 1u]);
+          if (g + 4 < kb1) {
+            load(g + 4);
+          } else if (t + t_step < tiles) {
+            set_tile(t + t_step);
+            load(kb0);
+          }
+        }
+      }
+      __syncwarp();
     }
     if (split > 1) {
       cluster_arrive();
@@ -523,7 +601,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     const int r = 32 * q4 + lane;              // token of the tile
     const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q4) << 16) + half * 64;
     int q = 0, s = 0;                          // next slot; stage of the next K block
-    uint32_t sph = 0, met = 0;
+    uint32_t sph = 0, met = 0, gi = 0;         // gi: groups of four K blocks so far
     bool ok = true;
     // Waits for the next K block's products.  The MMAs run at most NSLOT / NMAT K
     // blocks ahead, fewer than the stages: its barrier cannot be a phase further.
@@ -540,26 +618,6 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     for (int t = t_first; ok && t < tiles; t += t_step) {
       const F8Tile ti = tile_at(t);
       const bool any = 32 * q4 < ti.ntok;      // this warp's lanes hold tokens
-      // the token's and the weight blocks' scales, two K blocks at a time, the next
-      // two on their way
-      const float* ap = a.a_s + static_cast<size_t>(f8_row(a, ti, r)) * a.nk;
-      const float* wp[NMAT];
-#pragma unroll
-      for (int m = 0; m < NMAT; ++m) {
-        const int rb = GU ? ti.rblk : min(ti.rblk * NMAT + m, nrb - 1);
-        wp[m] = (GU && m ? a.w_s1 : a.w_s) + (static_cast<size_t>(ti.e) * nrb + rb) * a.nk;
-      }
-      float an[2], wn[NMAT][2];
-      auto load_scales = [&](int g) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int kb = min(g + c, kb1 - 1);
-          an[c] = ldg_here(ap + kb);
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m) wn[m][c] = ldg_here(wp[m] + kb);
-        }
-      };
-      if (any) load_scales(kb0);
 #pragma unroll
       for (int m = 0; m < NMAT; ++m)
 #pragma unroll
@@ -572,30 +630,42 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if (lane == 0) mbar_arrive(&slot_empty[q]);
         q = (q + 1) % C::NSLOT;
       };
+      auto free_scales = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[gi & 1u]);
+        ++gi;
+      };
       if (!any) {
-        for (int kb = kb0; kb < kb1 && (ok = next_block()); ++kb)
+        for (int kb = kb0; kb < kb1 && (ok = next_block()); ++kb) {
           for (int m = 0; m < NMAT; ++m) release();
+          if ((kb - kb0) % 4 == 3 || kb + 1 == kb1) {
+            if (!(ok = warp_wait(&sc_full[gi & 1u], (gi >> 1) & 1u, abort_flag, a.status))) break;
+            free_scales();
+          }
+        }
       } else {
         // 32 columns are on their way from tensor memory while 32 are added, the
         // next K block's first ones too
         uint32_t d[2][32];
         if ((ok = next_block())) tmem_ld32(tq + q * C::SLOT, d[0]);
-        for (int g = kb0; ok && g < kb1; g += 2) {
-          float sc[NMAT][2];
+        for (int g = kb0; ok && g < kb1; g += 4) {
+          if (!(ok = warp_wait(&sc_full[gi & 1u], (gi >> 1) & 1u, abort_flag, a.status))) break;
+          const float* scp = scales + (gi & 1u) * C::SCG + r;
+          float sc[4][NMAT];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int m = 0; m < NMAT; ++m) sc[m][c] = an[c] * wn[m][c];
-          if (g + 2 < kb1) load_scales(g + 2);
+            for (int m = 0; m < NMAT; ++m) sc[c][m] = scp[(c * NMAT + m) * 128];
+          free_scales();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < 4; ++c) {
             if (g + c >= kb1) break;
 #pragma unroll
             for (int m = 0; m < NMAT; ++m) {
               tmem_wait_ld32(d[0]);
               tmem_ld32(tq + q * C::SLOT + 32, d[1]);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) acc[m][0][x] = fmaf(__uint_as_float(d[0][x]), sc[m][c], acc[m][0][x]);
+              for (int x = 0; x < 32; ++x) acc[m][0][x] = fmaf(__uint_as_float(d[0][x]), sc[c][m], acc[m][0][x]);
               tmem_wait_ld32(d[1]);
               release();
               if (m + 1 < NMAT) {
@@ -605,7 +675,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                 tmem_ld32(tq + q * C::SLOT, d[0]);
               }
 #pragma unroll
-              for (int x = 0; x < 32; ++x) acc[m][1][x] = fmaf(__uint_as_float(d[1][x]), sc[m][c], acc[m][1][x]);
+              for (int x = 0; x < 32; ++x) acc[m][1][x] = fmaf(__uint_as_float(d[1][x]), sc[c][m], acc[m][1][x]);
             }
             if (!ok) break;
           }
@@ -687,15 +757,30 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         const int c = x % (NMAT * 128);
         const int col = ti.rblk * ROWS + c;
         const uint32_t base = smem_addr(smem);
-        for (int n = rank * PER + x / (NMAT * 128); n < ti.ntok; n += split * PER) {
-          float y = 0.f;
-          for (int p = 0; p < split; ++p) y += ld_cluster_f32(base + (c * C::TOT_LD + n) * 4, p);
-          if (col < a.R) {
-            const size_t at = static_cast<size_t>(ti.orow + n) * a.R + col;
-            if (a.out_f32)
-              static_cast<float*>(a.out)[at] = y;
-            else
-              static_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(y);
+        constexpr int UN = 4;                              // tokens in flight: up to 32 loads
+        for (int n0 = rank * PER + x / (NMAT * 128); n0 < ti.ntok; n0 += UN * split * PER) {
+          float v[UN][kF8MaxSplit];
+#pragma unroll
+          for (int p = 0; p < kF8MaxSplit; ++p)
+#pragma unroll
+            for (int u = 0; u < UN; ++u) {
+              const int n = n0 + u * split * PER;
+              if (p < split && n < ti.ntok) v[u][p] = ld_cluster_f32(base + (c * C::TOT_LD + n) * 4, p);
+            }
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            const int n = n0 + u * split * PER;
+            if (n < ti.ntok && col < a.R) {
+              float y = 0.f;
+#pragma unroll
+              for (int p = 0; p < kF8MaxSplit; ++p)
+                if (p < split) y += v[u][p];
+              const size_t at = static_cast<size_t>(ti.orow + n) * a.R + col;
+              if (a.out_f32)
+                static_cast<float*>(a.out)[at] = y;
+              else
+                static_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(y);
+            }
           }
         }
       }
