@@ -167,6 +167,23 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
                  "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31]));
 }
 
+// Two fp32 totals as a register pair: t += d * s in each half.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair2(uint32_t x, uint32_t y) {
+  f32x2 t;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "r"(x), "r"(y));
+  return t;
+}
+__device__ __forceinline__ void fma2(f32x2& t, uint32_t d0, uint32_t d1, f32x2 s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(t) : "l"(pair2(d0, d1)), "l"(s));
+}
+// The two halves of N / 2 pairs.
+template <int N>
+__device__ __forceinline__ void unpack_pairs(const f32x2 (&t)[N / 2], float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * i]), "=f"(v[2 * i + 1]) : "l"(t[i]));
+}
+
 // A load that stays where it is written (left to itself the compiler moves a
 // prefetch down to its use when registers are short).
 __device__ __forceinline__ float ldg_here(const float* p) {
@@ -614,7 +631,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       tc_fence_after();
       return true;
     };
-    float acc[NMAT][2][32];
+    f32x2 acc[NMAT][2][16];                    // 32 columns in pairs
     for (int t = t_first; ok && t < tiles; t += t_step) {
       const F8Tile ti = tile_at(t);
       const bool any = 32 * q4 < ti.ntok;      // this warp's lanes hold tokens
@@ -623,7 +640,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[m][c][i] = 0.f;
+          for (int i = 0; i < 16; ++i) acc[m][c][i] = 0ull;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -651,11 +668,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         for (int g = kb0; ok && g < kb1; g += 4) {
           if (!(ok = warp_wait(&sc_full[gi & 1u], (gi >> 1) & 1u, abort_flag, a.status))) break;
           const float* scp = scales + (gi & 1u) * C::SCG + r;
-          float sc[4][NMAT];
+          f32x2 sc[4][NMAT];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int m = 0; m < NMAT; ++m) sc[c][m] = scp[(c * NMAT + m) * 128];
+            for (int m = 0; m < NMAT; ++m) {
+              const uint32_t x = __float_as_uint(scp[(c * NMAT + m) * 128]);
+              sc[c][m] = pair2(x, x);
+            }
           free_scales();
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -665,7 +685,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               tmem_wait_ld32(d[0]);
               tmem_ld32(tq + q * C::SLOT + 32, d[1]);
 #pragma unroll
-              for (int x = 0; x < 32; ++x) acc[m][0][x] = fmaf(__uint_as_float(d[0][x]), sc[c][m], acc[m][0][x]);
+              for (int x = 0; x < 16; ++x) fma2(acc[m][0][x], d[0][2 * x], d[0][2 * x + 1], sc[c][m]);
               tmem_wait_ld32(d[1]);
               release();
               if (m + 1 < NMAT) {
@@ -675,7 +695,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                 tmem_ld32(tq + q * C::SLOT, d[0]);
               }
 #pragma unroll
-              for (int x = 0; x < 32; ++x) acc[m][1][x] = fmaf(__uint_as_float(d[1][x]), sc[c][m], acc[m][1][x]);
+              for (int x = 0; x < 16; ++x) fma2(acc[m][1][x], d[1][2 * x], d[1][2 * x + 1], sc[c][m]);
             }
             if (!ok) break;
           }
@@ -686,16 +706,18 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if (!any) continue;
         // h, the maximum of the token's 128 columns (64 in each of two threads),
         // codes and scale
-        float mx = 0.f;
+        float mx = 0.f, h[2][32];
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          float g[32];
+          unpack_pairs<32>(acc[0][c], g);
+          unpack_pairs<32>(acc[NMAT - 1][c], h[c]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float g = acc[0][c][i];
-            const float h = __fdividef(g, 1.0f + expf(-g)) * acc[NMAT - 1][c][i];
-            acc[0][c][i] = h;
-            mx = max_nan(mx, fabsf(h));
+            h[c][i] *= __fdividef(g[i], 1.0f + expf(-g[i]));
+            mx = max_nan(mx, fabsf(h[c][i]));
           }
+        }
         // the two warps of this lane quarter meet; with two sets of maxima a warp
         // writes a set again only after its partner came to the meeting in between
         float* rw = red + (met & 1u) * 256;
@@ -718,8 +740,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const float* h = &acc[0][c][16 * x + 4 * y];
-                w[y] = f8x4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+                const float* e = &h[c][16 * x + 4 * y];
+                w[y] = f8x4(e[0] * inv, e[1] * inv, e[2] * inv, e[3] * inv);
               }
               dst[2 * c + x] = make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -731,7 +753,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int col = ti.rblk * ROWS + m * 128 + half * 64 + c * 32;
-              f8_store_row<32>(a, static_cast<size_t>(ti.orow + r), col, acc[m][c]);
+              float v[32];
+              unpack_pairs<32>(acc[m][c], v);
+              f8_store_row<32>(a, static_cast<size_t>(ti.orow + r), col, v);
             }
         }
       } else if (r < NT) {
@@ -741,9 +765,12 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 2; ++c) {
+            float v[32];
+            unpack_pairs<32>(acc[m][c], v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) tot[(m * 128 + half * 64 + c * 32 + i) * C::TOT_LD + r] = acc[m][c][i];
+            for (int i = 0; i < 32; ++i) tot[(m * 128 + half * 64 + c * 32 + i) * C::TOT_LD + r] = v[i];
+          }
       }
     }
     if (split > 1) {
