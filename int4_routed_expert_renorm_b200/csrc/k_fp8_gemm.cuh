@@ -60,6 +60,7 @@ struct F8Args {
   const int32_t* perm;     // rows gathered by the copies: token perm / k of a pair (NULL: the pair's own row)
   int shared_row;          // first token row of every shared expert; -1: each has rows of its own, as out has
   int T, k, E, S, P;
+  int early;               // only a and a_s come from the kernel before this one
 };
 
 template <int NMAT, int NT>
@@ -77,13 +78,13 @@ struct F8Cfg {
   static constexpr int FIXED = 2 * SCG * 4 + 4 * 128 * 4 + META_INTS * 4 + 512;
   static constexpr int NST = (232448 - 1024 - FIXED) / (WSTAGE + ASTAGE);
   static constexpr size_t SMEM = 1024 + static_cast<size_t>(NST) * (WSTAGE + ASTAGE) + FIXED;
-  static constexpr int TOT_LD = NT + 1;                             // split K: totals [column][TOT_LD]
+  static constexpr int TOT_LD = NMAT * 128 + 1;                     // split K: totals [token][TOT_LD]
   static_assert(NT % 32 == 0 && NT <= 128, "a tile's tokens are tensor-memory lanes");
   static_assert(NST >= 3 && 2 * NST + NSLOT + 9 <= 60 && NST > NSLOT / NMAT, "stages");
   // the A operand's descriptor spans 128 rows whatever NT: the weight stages that
   // follow the token stages keep that inside the allocation
   static_assert(NST * WSTAGE >= 128 * 128 && ASTAGE % 1024 == 0, "operand extent");
-  static_assert(NMAT * 128 * TOT_LD * 4 <= NST * (WSTAGE + ASTAGE), "split-K totals fit the stages");
+  static_assert(NT * TOT_LD * 4 <= NST * (WSTAGE + ASTAGE), "split-K totals fit the stages");
 };
 
 // ------------------------------------------------------------------ PTX --
@@ -182,6 +183,17 @@ template <int N>
 __device__ __forceinline__ void unpack_pairs(const f32x2 (&t)[N / 2], float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * i]), "=f"(v[2 * i + 1]) : "l"(t[i]));
+}
+
+// x / (1 + exp(-x)) in four instructions.  The exponent's argument is rounded to
+// |x| 2^-24 of the result (a step of the e4m3 codes is 2^-3); the code runs once per
+// tile, so its length costs more than its arithmetic (single token, gate/up: 8.6 us
+// after the last product with expf and a division).
+__device__ __forceinline__ float silu(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return x * r;
 }
 
 // A load that stays where it is written (left to itself the compiler moves a
@@ -400,15 +412,19 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     prefetch_tensormap(&mb16);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
-  pdl_wait();
+  // The down launch follows the gate/up one, which passed its own wait before it
+  // let this one start: the plan and the weights are there, only h is not.
+  if (!a.early) pdl_wait();
   pdl_trigger();
   int n_seg = 0, U = 0, total_blocks;
   if (a.seg_off) {
     // token blocks of every segment, each of near-equal parts of at most NT tokens
+    // (the arrays have room for min(E, P) segments: no need to know U to load them)
+    const int most = min(a.E, a.P);
     U = __ldg(a.n_unique);
+    for (int i = threadIdx.x; i < most; i += blockDim.x) uniq[i] = static_cast<uint16_t>(__ldg(a.unique_ids + i));
+    for (int i = threadIdx.x; i <= most; i += blockDim.x) seg[i] = __ldg(a.seg_off + i);
     n_seg = U + a.S;
-    for (int i = threadIdx.x; i < U; i += blockDim.x) uniq[i] = static_cast<uint16_t>(__ldg(a.unique_ids + i));
-    for (int i = threadIdx.x; i <= U; i += blockDim.x) seg[i] = __ldg(a.seg_off + i);
     __syncthreads();
     int base = 0;
     for (int i0 = 0; i0 < n_seg; i0 += blockDim.x) {
@@ -440,45 +456,61 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   auto tile_at = [&](int t) { return f8_tile<NT>(a, blk_off, seg, uniq, n_seg, U, mbk, t); };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // ----------------------------------------------------- TMA producer
-      // the rows may come from an earlier kernel's plain stores
-      asm volatile("fence.proxy.async;" ::: "memory");
       uint32_t st = 0;
       bool ok = true;
+      auto copy_weights = [&](const F8Tile& ti, int kb, int s) {       // one lane
+        const int row0 = ti.e * a.R + ti.rblk * ROWS;
+        uint8_t* dst = w_stages + s * C::WSTAGE;
+        mbar_arrive_expect_tx(&full[s], C::WSTAGE + ti.npad * 128);
+        tma_load_2d(dst, &mw0, &full[s], kb * 128, row0);
+        if (NMAT == 2) tma_load_2d(dst + 128 * 128, GU ? &mw1 : &mw0, &full[s], kb * 128, GU ? row0 : row0 + 128);
+      };
+      // gathered rows: lane l takes rows 4l..4l+3
+      auto rows_of = [&](const F8Tile& ti) {
+        if (!ti.gather || 4 * lane >= ti.npad) return make_int4(0, 0, 0, 0);
+        return make_int4(f8_row(a, ti, 4 * lane), f8_row(a, ti, 4 * lane + 1), f8_row(a, ti, 4 * lane + 2),
+                         f8_row(a, ti, 4 * lane + 3));
+      };
+      auto copy_tokens = [&](const F8Tile& ti, int4 y, int kb, int s) {
+        uint8_t* d = a_stages + s * C::ASTAGE;
+        if (ti.gather) {
+          if (4 * lane < ti.npad) tma_gather4(d + lane * 512, &mgat, &full[s], kb * 128, y);
+        } else if (lane == 0) {
+          int row = ti.arow, rem = ti.npad;
+          if (rem >= 128) { tma_load_2d(d, &mb128, &full[s], kb * 128, row); rem = 0; }
+          if (rem >= 64) { tma_load_2d(d, &mb64, &full[s], kb * 128, row); rem -= 64; row += 64; d += 64 * 128; }
+          if (rem >= 32) { tma_load_2d(d, &mb32, &full[s], kb * 128, row); rem -= 32; row += 32; d += 32 * 128; }
+          if (rem >= 16) tma_load_2d(d, &mb16, &full[s], kb * 128, row);
+        }
+      };
+      // the first tile's weights are on their way while the rows are still written
+      const int ahead = a.early && t_first < tiles ? min(C::NST, kb1 - kb0) : 0;
+      if (ahead) {
+        const F8Tile ti = tile_at(t_first);
+        if (lane == 0)
+          for (int i = 0; i < ahead; ++i) copy_weights(ti, kb0 + i, i);
+        __syncwarp();
+        if (a.early) pdl_wait();
+        // the rows may come from an earlier kernel's plain stores
+        asm volatile("fence.proxy.async;" ::: "memory");
+        const int4 y = rows_of(ti);
+        for (int i = 0; i < ahead; ++i) copy_tokens(ti, y, kb0 + i, i);
+        st = ahead;
+      } else if (a.early) {
+        pdl_wait();
+      }
       for (int t = t_first; ok && t < tiles; t += t_step) {
         const F8Tile ti = tile_at(t);
-        const int row0 = ti.e * a.R + ti.rblk * ROWS;
-        // gathered rows: lane l takes rows 4l..4l+3 and 4(l+32)..: NT <= 256
-        int4 y0 = make_int4(0, 0, 0, 0);
-        if (ti.gather) {
-          if (4 * lane < ti.npad)
-            y0 = make_int4(f8_row(a, ti, 4 * lane), f8_row(a, ti, 4 * lane + 1), f8_row(a, ti, 4 * lane + 2),
-                           f8_row(a, ti, 4 * lane + 3));
-        }
-        for (int kb = kb0; kb < kb1; ++kb, ++st) {
+        const int4 y = rows_of(ti);
+        for (int kb = kb0 + (t == t_first ? ahead : 0); kb < kb1; ++kb, ++st) {
           const int s = static_cast<int>(st % C::NST);
           if (!(ok = warp_wait(&done[s], ((st / C::NST) & 1u) ^ 1u, abort_flag, a.status))) break;
-          uint8_t* dst = w_stages + s * C::WSTAGE;
-          uint8_t* bdst = a_stages + s * C::ASTAGE;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&full[s], C::WSTAGE + ti.npad * 128);
-            tma_load_2d(dst, &mw0, &full[s], kb * 128, row0);
-            if (NMAT == 2) tma_load_2d(dst + 128 * 128, GU ? &mw1 : &mw0, &full[s], kb * 128, GU ? row0 : row0 + 128);
-            if (!ti.gather) {
-              int row = ti.arow, rem = ti.npad;
-              uint8_t* d = bdst;
-              for (; rem >= 128; rem -= 128, row += 128, d += 128 * 128) tma_load_2d(d, &mb128, &full[s], kb * 128, row);
-              if (rem >= 64) { tma_load_2d(d, &mb64, &full[s], kb * 128, row); rem -= 64; row += 64; d += 64 * 128; }
-              if (rem >= 32) { tma_load_2d(d, &mb32, &full[s], kb * 128, row); rem -= 32; row += 32; d += 32 * 128; }
-              if (rem >= 16) tma_load_2d(d, &mb16, &full[s], kb * 128, row);
-            }
-          }
+          if (lane == 0) copy_weights(ti, kb, s);
           __syncwarp();
-          if (ti.gather) {
-            if (4 * lane < ti.npad) tma_gather4(bdst + lane * 512, &mgat, &full[s], kb * 128, y0);
-          }
+          copy_tokens(ti, y, kb, s);
         }
       }
       if (!ok && lane == 0) {
@@ -578,6 +610,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       };
       bool ok = true;
       uint32_t gi = 0;
+      if (a.early) pdl_wait();
       if (t_first < tiles) {
         set_tile(t_first);
         load(kb0);
@@ -612,7 +645,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     }
   } else {
     // ------------------------------------------------------------- totals
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int q4 = warp & 3;                   // TMEM lane quarter
     const int half = (warp - 4) >> 2;          // columns half * 64 .. + 63 of each 128
     const int r = 32 * q4 + lane;              // token of the tile
@@ -714,7 +747,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
           unpack_pairs<32>(acc[NMAT - 1][c], h[c]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            h[c][i] *= __fdividef(g[i], 1.0f + expf(-g[i]));
+            h[c][i] *= silu(g[i]);
             mx = max_nan(mx, fabsf(h[c][i]));
           }
         }
@@ -759,8 +792,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             }
         }
       } else if (r < NT) {
-        // split K: totals to shared memory (every copy and MMA of this CTA is done:
-        // its last slot was full)
+        // split K: totals to shared memory (every copy and MMA of this CTA is done),
+        // rows of odd length: no bank twice here, whole 128-byte lines to the peers
         float* tot = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int m = 0; m < NMAT; ++m)
@@ -769,7 +802,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
             float v[32];
             unpack_pairs<32>(acc[m][c], v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) tot[(m * 128 + half * 64 + c * 32 + i) * C::TOT_LD + r] = v[i];
+            for (int i = 0; i < 32; ++i) tot[r * C::TOT_LD + m * 128 + half * 64 + c * 32 + i] = v[i];
           }
       }
     }
@@ -792,7 +825,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
             for (int u = 0; u < UN; ++u) {
               const int n = n0 + u * split * PER;
-              if (p < split && n < ti.ntok) v[u][p] = ld_cluster_f32(base + (c * C::TOT_LD + n) * 4, p);
+              if (p < split && n < ti.ntok) v[u][p] = ld_cluster_f32(base + (n * C::TOT_LD + c) * 4, p);
             }
 #pragma unroll
           for (int u = 0; u < UN; ++u) {

@@ -379,6 +379,7 @@ coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims* dims, const coli_moe_we
   g.wide = 1;
   g.perm = nullptr;
   g.shared_row = -1;
+  g.early = 1;
   g.R = H;
   g.nk = I / kF8Block;
   const int64_t tiles_dn = blocks_ub * (H / kF8Block);
