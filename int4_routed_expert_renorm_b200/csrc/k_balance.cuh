@@ -183,7 +183,7 @@ struct BalOut {
 // grid is one cluster, which goes on to the results; otherwise they are left in
 // part_*.  Dynamic shared memory: (kBalWarps + 1) * E words.
 template <int NV, int VEC>
-__global__ void __launch_bounds__(kBalWarps * 32)
+__global__ void __launch_bounds__(kBalWarps * 32, NV <= 8 ? 2 : 1)
     balance_kernel(const float* __restrict__ logits, const float* __restrict__ bias, const int32_t* __restrict__ ids,
                    const uint8_t* __restrict__ mask, int T, int E, int k, int fused, float* __restrict__ part_p,
                    int32_t* __restrict__ part_c, int32_t* __restrict__ part_n, BalOut out,
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(512)
 // shared memory: kBalWarps * E floats (a row of the selected experts' terms per
 // warp, then the column sums).
 template <int NV, int VEC>
-__global__ void __launch_bounds__(kBalWarps * 32)
+__global__ void __launch_bounds__(kBalWarps * 32, NV <= 8 ? 2 : 1)
     balance_backward_kernel(const float* logits, const float* __restrict__ bias, const uint8_t* __restrict__ mask,
                             const int32_t* __restrict__ counts, const int32_t* __restrict__ n_live,
                             const float* __restrict__ grad_loss, const int32_t* __restrict__ ids,
