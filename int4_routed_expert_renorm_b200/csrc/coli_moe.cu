@@ -91,6 +91,7 @@ std::mutex g_mu;
 uint32_t* g_status_ptr[kMaxDevices] = {};
 int g_num_sms[kMaxDevices] = {};
 bool g_attr_done[kMaxDevices] = {};
+bool g_fp8_ok[kMaxDevices] = {};
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 // Shared memory of the 8-bit product's kernels.  Their setmaxnreg split hands out
@@ -131,6 +132,7 @@ bool balance_kernels_ready() {
 struct DevInfo {
   uint32_t* status;
   int sms;
+  bool fp8;   // the 8-bit product's kernels may run
 };
 
 coli_status dev_info(DevInfo* out) {
@@ -181,7 +183,8 @@ coli_status dev_info(DevInfo* out) {
     COLI_SET_SK_SMEM(1, 64, 8)
     COLI_SET_SK_SMEM(2, 64, 8)
 #undef COLI_SET_SK_SMEM
-    ok &= fp8_kernels_ready() && balance_kernels_ready();
+    ok &= balance_kernels_ready();
+    g_fp8_ok[dev] = fp8_kernels_ready();
     ok &= cudaFuncSetAttribute(logits_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
           cudaSuccess;
     ok &= cudaFuncSetAttribute(union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -208,6 +211,7 @@ coli_status dev_info(DevInfo* out) {
   }
   out->status = g_status_ptr[dev];
   out->sms = g_num_sms[dev];
+  out->fp8 = g_fp8_ok[dev];
   return COLI_OK;
 }
 

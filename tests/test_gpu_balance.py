@@ -278,3 +278,37 @@ def test_unaligned_rows_and_in_place_gradient(cm):
     cm.coli_moe_balance_backward(L, B, None, out[0], out[1], G, I, W, D, L, db, ws)
     torch.cuda.synchronize()
     _check((out[0].cpu(), int(out[1]), out[2].cpu().double(), float(out[3]), L.cpu().double(), db.cpu().double()), *x)
+
+
+@pytest.mark.parametrize("T", [255, 256, 257, 4096, 4737])
+def test_one_and_two_launches(cm, T):
+    """Up to 256 tokens one launch does everything, more take a second pass; 4736
+    tokens are one per warp."""
+    x = _inputs(T, 40, 3, T, live=0.9)
+    _check(_run(cm, *x), *x)
+
+
+def test_offsets_past_32_bits(cm):
+    """2.3e9 logits: the counts and the mean exactly as far as integers go, and rows
+    of the gradient from both ends."""
+    T, E, k = 2_200_003, 1024, 2
+    g = torch.Generator(device="cuda").manual_seed(60)
+    logits = torch.randn(T, E, device="cuda", generator=g)
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device="cuda", generator=g)
+    new = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    counts, n, P, loss = new(E, dtype=torch.int32), new(1, dtype=torch.int32), new(E), new(1)
+    ws = torch.empty(cm.coli_moe_balance_workspace_bytes(T, E), dtype=torch.uint8, device="cuda")
+    cm.coli_moe_balance(logits, None, ids, None, counts, n, P, loss, ws)
+    assert torch.equal(counts.long(), torch.bincount(ids.reshape(-1).long(), minlength=E)) and int(n) == T
+    assert abs(float(P.double().sum()) - 1) < 1e-4
+    grad = torch.ones(1, device="cuda")
+    rows = torch.tensor([0, 1, 2_097_151, 2_097_152, 2_200_002]).cuda()
+    l = logits[rows].double().cpu()
+    cm.coli_moe_balance_backward(logits, None, None, counts, n, grad, ids, None, None, logits, None, ws)
+    p = torch.softmax(l, 1)
+    f = counts.cpu().double() / (T * k)
+    want = E / T * p * (f - (p * f).sum(1, keepdim=True))
+    # as in _check, with |l - max| below 16: 80 half-steps of p, the rest of f and its sum
+    fc = (f - 1.0 / E).abs()
+    off = E / T * p * ((86 * U) * (f - (p * f).sum(1, keepdim=True)).abs() + 4 * U * fc + 128 * U * (p * fc).sum(1, keepdim=True))
+    assert (logits[rows].cpu().double() - want).abs().le(off + 2 * U * want.abs() + 1e-37).all()

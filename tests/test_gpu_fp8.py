@@ -391,3 +391,93 @@ def test_empty_batches(cm):
     cm.coli_fp8_matmul(torch.empty(0, 256, dtype=F8, device="cuda"), torch.empty(0, 2, device="cuda"), dev["gate_q"][0],
                        dev["gate_s"][0], torch.empty(0, 128, device="cuda"))
     assert cm.coli_moe_get_status() == (0, 0)
+
+
+def test_expert_ffn_with_no_expert_at_all(cm):
+    """Every id out of range and no shared expert: the residual comes back."""
+    for T in (3, 90):
+        dims = cm.dims_for(256, 128, 4, 2, 0, group=128, code_bits=8)
+        t = _experts(4, 0, 256, 128, 40)
+        g = torch.Generator().manual_seed(41)
+        xq, xs = ref.block_quantise(torch.randn(T, 256, generator=g, dtype=torch.float64), 1)
+        ids = torch.full((T, 2), -1, dtype=torch.int32)
+        w = torch.full((T, 2), 0.5)
+        r = torch.randn(T, 256, generator=g).to(torch.bfloat16)
+        out = _ffn(cm, dims, t, xq, xs, ids, w, r)
+        assert torch.equal(out.cpu(), r)
+        assert cm.coli_moe_get_status()[1] == cm._lib.COLI_FLAG_BAD_ID
+
+
+def test_expert_ffn_batch_boundaries(cm):
+    """32 tokens and fewer take one form, 33 another; segments of 127, 128, 129 and
+    256 tokens end on and beside a token block."""
+    H, I = 256, 128
+    for T, E, k, S in ((31, 3, 1, 1), (32, 3, 2, 0), (33, 3, 2, 1), (127, 1, 1, 0), (128, 1, 1, 1), (129, 1, 1, 0),
+                       (256, 2, 2, 0), (257, 1, 1, 2)):
+        dims = cm.dims_for(H, I, E, k, S, group=128, code_bits=8)
+        t = _experts(E, S, H, I, T)
+        g = torch.Generator().manual_seed(T)
+        xq, xs = ref.block_quantise(torch.randn(T, H, generator=g, dtype=torch.float64), 1)
+        _, ids, w = _routed(T, E, k, T)
+        out = _ffn(cm, dims, t, xq, xs, ids, w, None)
+        want, bound = ref.expert_ffn(dims, t, xq, xs, ids, w, None)
+        assert (out.cpu().double() - want).abs().le(bound).all(), (T, E, k, S)
+
+
+# ------------------------------------------------- offsets past 32 bits --
+
+def test_matmul_offsets_past_32_bits(cm):
+    """2.3e9 results: rows from the start, the middle and the end."""
+    M, N, K = 140_001, 16_392, 64
+    g = torch.Generator(device="cuda").manual_seed(50)
+    a = torch.randint(0, 120, (M, K), dtype=torch.uint8, device="cuda", generator=g).view(F8)
+    w = torch.randint(0, 120, (N, K), dtype=torch.uint8, device="cuda", generator=g).view(F8)
+    as_ = torch.rand(M, 1, device="cuda", generator=g)
+    ws = torch.rand(-(-N // 128), 1, device="cuda", generator=g)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    cm.coli_fp8_matmul(a, as_, w, ws, out)
+    rows = torch.tensor([0, 1, 65_535, 131_000, 131_071, 131_072, 140_000])
+    want, bound = ref.matmul(a[rows.cuda()].cpu(), as_[rows.cuda()].cpu(), w.cpu(), ws.cpu())
+    bound = bound + ref.UBF16 * (want.abs() + bound)
+    assert (out[rows.cuda()].cpu().double() - want).abs().le(bound).all()
+    assert cm.coli_moe_get_status() == (0, 0)
+
+
+def test_norm_offsets_past_32_bits(cm):
+    T, H = 70_003, 32_768
+    g = torch.Generator(device="cuda").manual_seed(51)
+    x = torch.randn(T, H, device="cuda", generator=g, dtype=torch.bfloat16)
+    q = torch.empty(T, H, dtype=F8, device="cuda")
+    sc = torch.empty(T, H // 128, device="cuda")
+    n = torch.empty_like(x)
+    cm.coli_add_rmsnorm_fp8(x, None, None, 1e-6, None, n, q, sc)
+    rows = torch.tensor([0, 65_535, 65_536, 70_002]).cuda()
+    v = x[rows].cpu().double()
+    want = v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6)
+    assert (n[rows].cpu().double() - want).abs().le((88 * U + ref.UBF16) * want.abs() + 1e-37).all()
+    # half an e4m3 step of a normal value, half the smallest step (2^-10 scales) below
+    deq = ref.decode(q[rows]) * ref.spread(sc[rows].cpu().double(), H, 1)
+    assert (deq - want).abs().le(2.0 ** -4 * want.abs() * (1 + 200 * U) + 2.0 ** -10 * ref.spread(sc[rows].cpu().double(), H, 1)).all()
+
+
+def test_expert_ffn_offsets_past_32_bits(cm):
+    """2.2e9 values of y and of the gathered codes: tokens from both ends."""
+    T, E, k, H, I = 44_001, 8, 8, 6_144, 128
+    dims = cm.dims_for(H, I, E, k, 0, group=128, code_bits=8)
+    t = _experts(E, 0, H, I, 52)
+    dev = {m: v.cuda() for m, v in t.items()}
+    g = torch.Generator(device="cuda").manual_seed(53)
+    xq = torch.randint(0, 120, (T, H), dtype=torch.uint8, device="cuda", generator=g)
+    xq = (xq + 128 * torch.randint(0, 2, (T, H), dtype=torch.uint8, device="cuda", generator=g)).view(F8)
+    xs = 0.01 * torch.rand(T, H // 128, device="cuda", generator=g)
+    top, ids = torch.topk(torch.randn(T, E, device="cuda", generator=g), k, dim=1)
+    ids, w = ids.to(torch.int32), torch.softmax(top, 1)
+    arrays = ref.union(ids, E)
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(cm.coli_moe_fp8_workspace_bytes(dims, T), dtype=torch.uint8, device="cuda")
+    cm.coli_moe_expert_ffn_fp8(dims, cm.fp8_weights(**dev), xq, xs, ids, w, *arrays, None, out, ws)
+    rows = torch.tensor([0, 1, 22_000, 43_999, 44_000]).cuda()
+    want, bound = ref.expert_ffn(dims, t, xq[rows].cpu(), xs[rows].cpu(), ids[rows].cpu(), w[rows].cpu(), None)
+    err = (out[rows].cpu().double() - want).abs()
+    assert err.le(bound).all(), float((err / bound).max())
+    assert cm.coli_moe_get_status() == (0, 0)
