@@ -63,7 +63,8 @@
  *     I == 128; group == 64 with H % 512 == 0, I % 512 == 0; int8 codes
  *     need I % 256 == 0 (group 32) or I % 512 == 0 (group 64); and for all
  *     1 <= k <= min(E, 32), E <= 1024, 0 <= S <= 4, T >= 0, T*k <= 2^24.
- *     Anything else returns COLI_ERR_UNSUPPORTED.
+ *     Anything else returns COLI_ERR_UNSUPPORTED.  (The 8-bit floating-point
+ *     calls have their own set, stated at each.)
  *   - Thread safety: calls may be made concurrently from several host
  *     threads on different streams; the device status word is shared by all
  *     of them.
@@ -89,8 +90,9 @@ typedef enum {
 } coli_status;
 
 /* Device status bits (coli_moe_get_status). */
-#define COLI_FLAG_NONFINITE 0x1u  /* a logit was NaN or +inf, or a selected logit was -inf */
-#define COLI_FLAG_BAD_ID    0x2u  /* an expert id outside [0, E) reached the union */
+#define COLI_FLAG_NONFINITE 0x1u  /* a logit was NaN or +inf, or a selected logit was -inf; or a row of
+                                   * coli_add_rmsnorm_fp8 has no finite sum of squares */
+#define COLI_FLAG_BAD_ID    0x2u  /* an expert id outside [0, E) reached the union or coli_moe_balance */
 #define COLI_FLAG_TIMEOUT   0x4u  /* a bounded pipeline wait expired; outputs are undefined */
 #define COLI_FLAG_RANGE     0x8u  /* the prefill form met an expert input or h value of magnitude
                                    * 65536 or more, which its fp16 operands cannot hold; outputs

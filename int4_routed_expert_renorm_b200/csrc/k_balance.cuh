@@ -19,7 +19,9 @@
 // memory; larger batches write their blocks' sums to the workspace and a second
 // launch adds them.
 // Bound by HBM (4 bytes per logit read forward; 4 read and 4 written backward) for
-// large batches and by latency for small ones.
+// large batches and by latency for small ones.  65536 x 256, top-8: 69 us for both
+// passes with the bias gradient (210 MB; 27 + 10 us forward, 40 + 6 backward, each
+// launch alone and cold).
 #pragma once
 #include "common.cuh"
 

