@@ -22,16 +22,18 @@
 //     slot of tensor memory, a fresh accumulator per K block;
 //   * warps 4..11 read the slot (tcgen05.ld), multiply-add it into fp32 totals in
 //     registers and free the slot.  A thread owns one token and half of the
-//     columns: 128 totals, hence the register split below.
+//     columns, of each weight block or of the pair: 128 totals, hence the register
+//     split below;
+//   * warps 2 and 3 keep the scales of the next four K blocks in shared memory.
 // The gate/up launch ends a tile with h = silu(g) u, the token's maximum over the
 // tile's 128 columns (two threads, through shared memory) and e4m3 codes with
 // their scale: g and u never leave the SM.
 // A operand rows past the tile's tokens are whatever shared memory holds; they
 // only reach tensor-memory lanes that nothing reads.
-// Measured on one B200: 8192 x 12288 x 6144 in 774 us (1.60 PFLOP/s; a K block of a
-// tile takes 1240 cycles, its MMAs 512, its copies 1035, its totals 1050); 1 x 4096 x
-// 6144 in 11 us; the FFN of a 256-expert layer (H 6144, I 2048, top-8, one shared)
-// in 76 us for 1 token, 1.60 ms for 256 (HBM floor 1.48), 2.97 ms for 4096.
+// Measured on one B200: 8192 x 12288 x 6144 in 748 us (1.65 PFLOP/s; a K block of a
+// tile takes 1130 cycles, its MMAs 512, its copies alone 1035); 1 x 4096 x 6144 in
+// 11 us; the FFN of a 256-expert layer (H 6144, I 2048, top-8, one shared) in 76 us
+// for 1 token, 1.60 ms for 256 (HBM floor 1.48), 2.93 ms for 4096.
 #pragma once
 #include <type_traits>
 
@@ -85,7 +87,7 @@ struct F8Cfg {
   static constexpr size_t SMEM = 1024 + static_cast<size_t>(NST) * (WSTAGE + ASTAGE) + FIXED;
   static constexpr int TOT_LD = NMAT * 128 + 1;                     // split K: totals [token][TOT_LD]
   static_assert(NT % 32 == 0 && NT <= 128, "a tile's tokens are tensor-memory lanes");
-  static_assert(NST >= 3 && 2 * NST + NSLOT + 9 <= 60 && NST > NSLOT / NMAT, "stages");
+  static_assert(NST >= 3 && 2 * NST + NSLOT + 11 <= 60 && NST > NSLOT / NMAT, "stages");
   // the A operand's descriptor spans 128 rows whatever NT: the weight stages that
   // follow the token stages keep that inside the allocation
   static_assert(NST * WSTAGE >= 128 * 128 && ASTAGE % 1024 == 0, "operand extent");
@@ -180,7 +182,7 @@ __device__ __forceinline__ void fma2(f32x2& t, uint32_t d0, uint32_t d1, f32x2 s
 }
 // The two halves of N / 2 pairs.
 template <int N>
-__device__ __forceinline__ void unpack_pairs(const f32x2 (&t)[N / 2], float (&v)[N]) {
+__device__ __forceinline__ void unpack_pairs(const f32x2* t, float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N / 2; ++i) asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * i]), "=f"(v[2 * i + 1]) : "l"(t[i]));
 }
@@ -288,11 +290,11 @@ __device__ __forceinline__ int f8_row(const F8Args& a, const F8Tile& ti, int n) 
 }
 
 // The expert input of a routed batch in pair order: row i < P is the codes and
-// scales of token perm[i] / k, the `extra` rows after them
-// the tokens in order (T of them for the shared experts, or none).  One warp per row, 16-byte moves.  For more than 32 tokens
-// this pays: copies that gather four rows each bring 128 rows in 1800 cycles, a
-// plain 128-row copy in 1000 (gate/up of 4096 tokens 2.84 against 1.73 ms, and this
-// kernel takes 0.07).
+// scales of token perm[i] / k, the `extra` rows after them the tokens in order (T of
+// them for the shared experts, or none).  One warp per row, 16-byte moves.  For more
+// than 32 tokens this pays: copies that gather four rows each bring 128 rows in 1800
+// cycles, a plain 128-row copy in 1000 (gate/up of 4096 tokens 2.84 against 1.76 ms,
+// and this kernel takes 0.07).
 __global__ void __launch_bounds__(256) f8_gather_kernel(const uint8_t* __restrict__ x, const float* __restrict__ x_s,
                                                         const int32_t* __restrict__ perm, int k, int P, int extra, int T, int H,
                                                         uint8_t* __restrict__ xg, float* __restrict__ sg) {
@@ -380,13 +382,18 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   uint64_t* full = bars;
   uint64_t* done = full + C::NST;                 // the stage's MMAs are complete
   uint64_t* slot_empty = done + C::NST;
-  uint64_t* pair_bar = slot_empty + C::NSLOT;      // [4]: the two warps of a lane quarter
+  uint64_t* first_done = slot_empty + C::NSLOT;    // [2]: a K block's first weight block is multiplied (BYMAT)
+  uint64_t* pair_bar = first_done + 2;             // [4]: the two warps of a lane quarter
   uint64_t* sc_full = pair_bar + 4;                // [2]: a group's scales are written
   uint64_t* sc_empty = sc_full + 2;                // and read
   uint64_t* mma_done = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
   int* scratch = reinterpret_cast<int*>(red);     // 33 ints, before the tiles
+  // A dense or down tile of two weight blocks: each block has four warps of totals
+  // of its own; otherwise all eight share every block's columns.
+  constexpr bool BYMAT = NMAT == 2 && !GU;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -395,10 +402,11 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       mbar_init(&done[q], 1);
     }
     for (int q = 0; q < C::NSLOT; ++q) {
-      mbar_init(&slot_empty[q], 8);
+      mbar_init(&slot_empty[q], BYMAT ? 4 : 8);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&pair_bar[q], 2);
     for (int q = 0; q < 2; ++q) {
+      mbar_init(&first_done[q], 1);
       mbar_init(&sc_full[q], 2);
       mbar_init(&sc_empty[q], 8);
     }
@@ -553,6 +561,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
               }
               mma_f8_ss(tbase + q * C::SLOT, adesc + kk * 2, wdesc + m * 1024 + kk * 2, idesc, kk != 0, leader);
             }
+            if (BYMAT && m == 0) tc_commit_on(&first_done[q >> 1], leader);
             q = q1;
             qph = qph1;
           }
@@ -647,38 +656,44 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     // ------------------------------------------------------------- totals
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int q4 = warp & 3;                   // TMEM lane quarter
-    const int half = (warp - 4) >> 2;          // columns half * 64 .. + 63 of each 128
+    // BYMAT: warps 4..7 take the first weight block's 128 columns and warps 8..11 the
+    // second one's, each as soon as it is multiplied, so that the two warps of a
+    // scheduler wait and add in turn (K block of a dense product 1240 -> 1133 cycles;
+    // for gate/up it loses: u then has to travel, 1.67 against 1.78 ms).  Otherwise a
+    // warp takes half of each block's columns.
+    const int half = (warp - 4) >> 2;
+    constexpr int MH = BYMAT ? 1 : NMAT, NCOL = BYMAT ? 128 : 64, NB = NCOL / 16;
     const int r = 32 * q4 + lane;              // token of the tile
-    const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q4) << 16) + half * 64;
-    int q = 0, s = 0;                          // next slot; stage of the next K block
+    const uint32_t tq = tbase + (static_cast<uint32_t>(32 * q4) << 16) + (BYMAT ? 0 : half * 64);
+    int q = BYMAT ? half : 0;                  // next slot
+    int s = 0;                                 // stage of the next K block
     uint32_t sph = 0, met = 0, gi = 0;         // gi: groups of four K blocks so far
     bool ok = true;
     // Waits for the next K block's products.  The MMAs run at most NSLOT / NMAT K
-    // blocks ahead, fewer than the stages: its barrier cannot be a phase further.
+    // blocks ahead, fewer than the stages: no barrier can be a phase further.
     auto next_block = [&]() -> bool {
-      if (!warp_wait(&done[s], sph, abort_flag, a.status)) return false;
-      if (++s == C::NST) {
+      const bool first = BYMAT && half == 0;
+      if (!warp_wait(first ? &first_done[s] : &done[s], sph, abort_flag, a.status)) return false;
+      if (++s == (first ? 2 : C::NST)) {
         s = 0;
         sph ^= 1u;
       }
       tc_fence_after();
       return true;
     };
-    f32x2 acc[NMAT][2][16];                    // 32 columns in pairs
+    f32x2 acc[MH][NCOL / 2];                   // columns in pairs
     for (int t = t_first; ok && t < tiles; t += t_step) {
       const F8Tile ti = tile_at(t);
       const bool any = 32 * q4 < ti.ntok;      // this warp's lanes hold tokens
 #pragma unroll
-      for (int m = 0; m < NMAT; ++m)
+      for (int m = 0; m < MH; ++m)
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[m][c][i] = 0ull;
+        for (int i = 0; i < NCOL / 2; ++i) acc[m][i] = 0ull;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&slot_empty[q]);
-        q = (q + 1) % C::NSLOT;
+        q = (q + (BYMAT ? 2 : 1)) % C::NSLOT;
       };
       auto free_scales = [&]() {
         __syncwarp();
@@ -687,7 +702,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       };
       if (!any) {
         for (int kb = kb0; kb < kb1 && (ok = next_block()); ++kb) {
-          for (int m = 0; m < NMAT; ++m) release();
+          for (int m = 0; m < MH; ++m) release();
           if ((kb - kb0) % 4 == 3 || kb + 1 == kb1) {
             if (!(ok = warp_wait(&sc_full[gi & 1u], (gi >> 1) & 1u, abort_flag, a.status))) break;
             free_scales();
@@ -703,27 +718,27 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         if ((ok = next_block())) tmem_ld16(tq + q * C::SLOT, d[0]);
         for (int g = kb0; ok && g < kb1; g += 4) {
           if (!(ok = warp_wait(&sc_full[gi & 1u], (gi >> 1) & 1u, abort_flag, a.status))) break;
-          const float* scp = scales + (gi & 1u) * C::SCG + r;
+          const float* scp = scales + (gi & 1u) * C::SCG + (BYMAT ? half * 128 : 0) + r;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             if (g + c >= kb1) break;
-            float sm[NMAT];
+            float sm[MH];
 #pragma unroll
-            for (int m = 0; m < NMAT; ++m) sm[m] = scp[(c * NMAT + m) * 128];
+            for (int m = 0; m < MH; ++m) sm[m] = scp[(c * NMAT + m) * 128];
             if (c == 3 || g + c + 1 == kb1) free_scales();
 #pragma unroll
-            for (int m = 0; m < NMAT; ++m) {
+            for (int m = 0; m < MH; ++m) {
               const f32x2 s2 = pair2(__float_as_uint(sm[m]), __float_as_uint(sm[m]));
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
+              for (int b = 0; b < NB; ++b) {
                 uint32_t(&cur)[16] = d[b & 1];
                 uint32_t(&nxt)[16] = d[(b + 1) & 1];
                 tmem_wait_ld16(cur);
-                if (b < 3) {
+                if (b + 1 < NB) {
                   tmem_ld16(tq + q * C::SLOT + 16 * (b + 1), nxt);
                 } else {
                   release();
-                  if (m + 1 < NMAT) {
+                  if (m + 1 < MH) {
                     tmem_ld16(tq + q * C::SLOT, nxt);
                   } else if (g + c + 1 < kb1) {
                     if (!(ok = next_block())) break;
@@ -731,8 +746,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
                   }
                 }
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  fma2(acc[m][b / 2][8 * (b % 2) + x], cur[2 * x], cur[2 * x + 1], s2);
+                for (int x = 0; x < 8; ++x) fma2(acc[m][8 * b + x], cur[2 * x], cur[2 * x + 1], s2);
               }
               if (!ok) break;
             }
@@ -749,8 +763,8 @@ __global__ void __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float g[32];
-          unpack_pairs<32>(acc[0][c], g);
-          unpack_pairs<32>(acc[NMAT - 1][c], h[c]);
+          unpack_pairs<32>(&acc[0][16 * c], g);
+          unpack_pairs<32>(&acc[MH - 1][16 * c], h[c]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             h[c][i] *= silu(g[i]);
@@ -788,28 +802,23 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       } else if (split == 1) {
         if (r < ti.ntok) {
 #pragma unroll
-          for (int m = 0; m < NMAT; ++m)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int col = ti.rblk * ROWS + m * 128 + half * 64 + c * 32;
-              float v[32];
-              unpack_pairs<32>(acc[m][c], v);
-              f8_store_row<32>(a, static_cast<size_t>(ti.orow + r), col, v);
-            }
+          for (int c = 0; c < NCOL / 32; ++c) {
+            float v[32];
+            unpack_pairs<32>(&acc[0][16 * c], v);
+            f8_store_row<32>(a, static_cast<size_t>(ti.orow + r), ti.rblk * ROWS + half * NCOL + c * 32, v);
+          }
         }
       } else if (r < NT) {
         // split K: totals to shared memory (every copy and MMA of this CTA is done),
         // rows of odd length: no bank twice here, whole 128-byte lines to the peers
         float* tot = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int m = 0; m < NMAT; ++m)
+        for (int c = 0; c < NCOL / 32; ++c) {
+          float v[32];
+          unpack_pairs<32>(&acc[0][16 * c], v);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float v[32];
-            unpack_pairs<32>(acc[m][c], v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) tot[r * C::TOT_LD + m * 128 + half * 64 + c * 32 + i] = v[i];
-          }
+          for (int i = 0; i < 32; ++i) tot[r * C::TOT_LD + half * NCOL + c * 32 + i] = v[i];
+        }
       }
     }
     if (split > 1) {
