@@ -369,7 +369,11 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 _ANY = None
 
 
-def _refuse(specs, dev):
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _refuse(specs):
     """Why _args refused its arguments: types and sizes first, then layout and device."""
     given = [x for x in specs if x[1] is not None]
     for name, t, types, n, at_least in given:
@@ -380,39 +384,47 @@ def _refuse(specs, dev):
             raise ValueError(f"{name}: {t.numel()} elements, the call needs {'at least ' if at_least else ''}{n}")
     for name, t, *_ in given:
         _ptr(t)
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: a tensor on {t.device}, but the current device is cuda:{dev}")
-    raise ValueError("no CUDA device is initialised")
+    for name, t, *_ in given:
+        if t.get_device() != _current_device():
+            raise ValueError(f"{name}: a tensor on {t.device}, but the current device is cuda:{_current_device()}")
+    raise ValueError("arguments refused")
 
 
 def _args(*specs):
     """Data pointers of (name, tensor, types, elements, at_least) arguments (None
-    -> NULL): dense tensors of these types and sizes on the current device, where
-    the call launches."""
-    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    -> NULL) and their device: dense tensors of these types and sizes on the
+    current device, where the call launches."""
+    dev = None
     out = []
-    for name, t, types, n, at_least in specs:
+    for _, t, types, n, at_least in specs:
         if t is None:
             out.append(None)
             continue
-        if ((types is not None and t.dtype not in types) or (n is not None and (t.numel() < n if at_least else t.numel() != n))
-                or not t.is_contiguous() or t.get_device() != dev or dev < 0):
-            _refuse(specs, dev)
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        if (d != dev or d < 0 or not t.is_contiguous() or (types is not None and t.dtype not in types)
+                or (n is not None and (t.numel() < n if at_least else t.numel() != n))):
+            _refuse(specs)
         out.append(t.data_ptr())
+    if dev != _current_device():
+        _refuse(specs)
+    out.append(dev)
     return out
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, dev):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _current_stream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t, name: str):
     """The shape of a 2-D tensor."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs two dimensions")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: shape {tuple(shape)}, the call needs two dimensions")
+    return shape
 
 
 def coli_moe_balance_workspace_bytes(t_max: int, n_experts: int) -> int:
@@ -429,7 +441,7 @@ def coli_moe_balance(logits, bias, topk_ids, mask, counts, n_live, prob_mean, lo
               ("counts", counts, _I32, E, False), ("n_live", n_live, _I32, 1, False),
               ("prob_mean", prob_mean, _F32, E, False), ("loss", loss, _F32, 1, False), ("ws", ws, _ANY, None, False))
     st = _lib.coli_moe_balance(p[0], p[1], p[2], p[3], T, E, k, p[4], p[5], p[6], p[7], p[8], ws.nbytes,
-                               _raw_stream(stream))
+                               _raw_stream(stream, p[-1]))
     if st:
         _check(st, "coli_moe_balance")
 
@@ -453,7 +465,7 @@ def coli_moe_balance_backward(logits, bias, mask, counts, n_live, grad_loss, top
               ("d_logits", d_logits, _F32, T * E, False), ("d_bias", d_bias, _F32, E, False),
               ("ws", ws, _ANY, None, False))
     st = _lib.coli_moe_balance_backward(p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], T, E, k, p[9], p[10], p[11],
-                                        ws.nbytes, _raw_stream(stream))
+                                        ws.nbytes, _raw_stream(stream, p[-1]))
     if st:
         _check(st, "coli_moe_balance_backward")
 
@@ -466,7 +478,7 @@ def coli_add_rmsnorm_fp8(x, residual, weight, eps: float, sum_out, norm_out, q, 
     p = _args(("x", x, _BF16, None, False), ("residual", residual, _BF16, n, False), ("weight", weight, _BF16, H, False),
               ("sum_out", sum_out, _BF16, n, False), ("norm_out", norm_out, _BF16, n, False), ("q", q, _E4M3, n, False),
               ("q_scale", q_scale, _F32, T * (H // 128), False))
-    st = _lib.coli_add_rmsnorm_fp8(p[0], p[1], p[2], eps, T, H, p[3], p[4], p[5], p[6], _raw_stream(stream))
+    st = _lib.coli_add_rmsnorm_fp8(p[0], p[1], p[2], eps, T, H, p[3], p[4], p[5], p[6], _raw_stream(stream, p[-1]))
     if st:
         _check(st, "coli_add_rmsnorm_fp8")
 
@@ -481,7 +493,8 @@ def coli_fp8_matmul(a, a_scale, w, w_scale, out, stream=None):
     f32 = out.dtype == torch.float32
     p = _args(("a", a, _E4M3, None, False), ("a_scale", a_scale, _F32, M * nk, False), ("w", w, _E4M3, N * K, False),
               ("w_scale", w_scale, _F32, -(-N // 128) * nk, False), ("out", out, _F32 if f32 else _BF16, M * N, False))
-    st = _lib.coli_fp8_matmul(p[0], p[1], p[2], p[3], M, N, K, p[4], COLI_FP8_OUT_F32 if f32 else 0, _raw_stream(stream))
+    st = _lib.coli_fp8_matmul(p[0], p[1], p[2], p[3], M, N, K, p[4], COLI_FP8_OUT_F32 if f32 else 0,
+                              _raw_stream(stream, p[-1]))
     if st:
         _check(st, "coli_fp8_matmul")
 
@@ -506,6 +519,6 @@ def coli_moe_expert_ffn_fp8(dims, weights, x, x_scale, topk_ids, topk_w, unique_
               ("pair_pos", pair_pos, _I32, P, True), ("residual", residual, _BF16, T * H, False),
               ("out", out, _BF16, T * H, False), ("ws", ws, _ANY, None, False))
     st = _lib.coli_moe_expert_ffn_fp8(ctypes.byref(dims), ctypes.byref(weights), p[0], p[1], T, p[2], p[3], p[4], p[5],
-                                      p[6], p[7], p[8], p[9], p[10], p[11], ws.nbytes, _raw_stream(stream))
+                                      p[6], p[7], p[8], p[9], p[10], p[11], ws.nbytes, _raw_stream(stream, p[-1]))
     if st:
         _check(st, "coli_moe_expert_ffn_fp8")

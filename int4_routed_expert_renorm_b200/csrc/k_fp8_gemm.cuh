@@ -15,9 +15,9 @@
 // tile is up to NT tokens x NMAT * 128 weight rows: gate and up blocks of the same
 // 128 columns of h, or neighbouring blocks of one matrix.  Per 128-wide K block:
 //   * warp 0 brings the weight blocks (128 x 128 bytes each) and the token rows
-//     into a stage of shared memory by TMA (128B swizzle); rows of a routed segment
-//     are gathered four at a time by their token index, so the batch is never
-//     copied into pair order;
+//     into a stage of shared memory by TMA (128B swizzle); in batches of up to 32
+//     tokens the rows of a routed segment are gathered four at a time by their
+//     token index, larger ones are copied into pair order first;
 //   * warp 1 multiplies them (four tcgen05.mma kind::f8f6f4, K = 32 each) into a
 //     slot of tensor memory, a fresh accumulator per K block;
 //   * warps 4..11 read the slot (tcgen05.ld), multiply-add it into fp32 totals in
