@@ -4,15 +4,20 @@
 //   n = s * (mean(s^2) + eps)^(-1/2) * g (g = 1 without a weight), in fp32
 //   per 128 columns: c = max(max|n| / 448, 2^-126),  q = e4m3(n / c)
 // 448 is e4m3's largest value, so the block's largest |n| lands on it.  The
-// codes are rounded from the fp32 n, not from its bf16 copy.  The floor 2^-126
+// codes are rounded from the unrounded n, not from its bf16 copy.  The floor 2^-126
 // keeps the scale a normal number for blocks of zeros.
+// The root cancels in n / c: q = e4m3(s g * (448 / max|s g|)).  s g (two bf16 numbers)
+// is exact in fp32, so a code sees two roundings before its own, the block's quotient
+// and the product; from n and c it would see six, and a value near a border of the
+// codes would land on the wrong side more often.  (A division per value would leave
+// one, and costs 176 against 141 us at 16384 x 6144.)
 //
 // One block of 256 threads per row; a thread holds 8 consecutive values per 2048
 // columns (one 16-byte load), so a 128-column block is 16 neighbouring lanes and
 // its maximum a 4-step shuffle.  The row is read once and stays in registers.
 // Bound by HBM for large batches (9.03 bytes per value with everything written)
 // and by latency for single tokens.  16384 x 6144 with residual, weight and all
-// outputs: 137 us, 6.64 TB/s.
+// outputs: 141 us, 6.45 TB/s (five blocks per SM; 146 us with four).
 #pragma once
 #include <cuda_fp8.h>
 
@@ -52,7 +57,7 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 // NC: 2048-column steps of a row (H <= 2048 * NC).  x, residual and sum_out may
 // be the same buffer: a thread reads its values before it writes them.
 template <int NC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, NC <= 3 ? 5 : 1)
     add_rmsnorm_fp8_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,
                            int H, uint16_t* sum_out, uint16_t* __restrict__ norm_out, uint8_t* __restrict__ q,
                            float* __restrict__ q_scale, uint32_t* __restrict__ status) {
@@ -110,27 +115,53 @@ __global__ void __launch_bounds__(256)
     uint4 gw = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);   // bf16 ones
     if (weight && c < H) gw = __ldg(reinterpret_cast<const uint4*>(weight + c));
     const uint32_t g[4] = {gw.x, gw.y, gw.z, gw.w};
-    float n[8];
-    float m = 0.f;
+    float y[8];
+    float m = 0.f;            // max|s g|
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      n[2 * k] = __uint_as_float(w[k] << 16) * rs * __uint_as_float(g[k] << 16);
-      n[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * rs * __uint_as_float(g[k] & 0xffff0000u);
-      m = max_nan(m, max_nan(fabsf(n[2 * k]), fabsf(n[2 * k + 1])));
+      y[2 * k] = __uint_as_float(w[k] << 16) * __uint_as_float(g[k] << 16);
+      y[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * __uint_as_float(g[k] & 0xffff0000u);
+      m = max_nan(m, max_nan(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float rn = rs, mn = m * rs;      // n = y * rn, max|n|
+    // s g at fp32's ends, where it is no longer exact (zeros and NaN among them): y becomes n
+    const bool exact = m > 1e-25f && m < 1e35f;
+    if (__any_sync(0xffffffffu, !exact)) {
+      float z[8];
+      float mz = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        z[2 * k] = __uint_as_float(w[k] << 16) * rs * __uint_as_float(g[k] << 16);
+        z[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u) * rs * __uint_as_float(g[k] & 0xffff0000u);
+        mz = max_nan(mz, max_nan(fabsf(z[2 * k]), fabsf(z[2 * k + 1])));
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mz = max_nan(mz, __shfl_xor_sync(0xffffffffu, mz, o));
+      if (!exact) {
+        rn = 1.0f;
+        mn = mz;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = z[k];
+      }
+    }
     if (c < H) {
       float inv;
-      const float sc = f8_scale(m, &inv);
+      const float sc = f8_scale(mn, &inv);
       if ((lane & 15) == 0) q_scale[static_cast<size_t>(blockIdx.x) * nb + c / kF8Block] = sc;
+      const float by = exact && sc > kF8MinScale ? kF8Max / m : rn * inv;
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = y[k] * by;
       uint2 o;
-      o.x = f8x4(n[0] * inv, n[1] * inv, n[2] * inv, n[3] * inv);
-      o.y = f8x4(n[4] * inv, n[5] * inv, n[6] * inv, n[7] * inv);
+      o.x = f8x4(v[0], v[1], v[2], v[3]);
+      o.y = f8x4(v[4], v[5], v[6], v[7]);
       *reinterpret_cast<uint2*>(q + row + c) = o;
       if (norm_out)
         *reinterpret_cast<uint4*>(norm_out + row + c) =
-            make_uint4(bf16x2(n[0], n[1]), bf16x2(n[2], n[3]), bf16x2(n[4], n[5]), bf16x2(n[6], n[7]));
+            make_uint4(bf16x2(y[0] * rn, y[1] * rn), bf16x2(y[2] * rn, y[3] * rn), bf16x2(y[4] * rn, y[5] * rn),
+                       bf16x2(y[6] * rn, y[7] * rn));
     }
   }
 }

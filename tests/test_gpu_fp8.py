@@ -481,3 +481,30 @@ def test_expert_ffn_offsets_past_32_bits(cm):
     err = (out[rows].cpu().double() - want).abs()
     assert err.le(bound).all(), float((err / bound).max())
     assert cm.coli_moe_get_status() == (0, 0)
+
+
+def test_norm_codes_are_the_nearest(cm):
+    """Away from the ends of fp32 a code is the nearest one to the exact ratio 448 s g
+    / max|s g|: two fp32 roundings before the code's own (the quotient 448 / max, the
+    product), half a step 2^-24 each, (1 + 2^-24)^2 - 1 < 2.01 * 2^-24: only a ratio
+    within that of a border may land on its other side."""
+    g = torch.Generator().manual_seed(70)
+    x = (3 * torch.randn(600, 6144, generator=g)).to(torch.bfloat16)
+    w = (1 + 0.3 * torch.randn(6144, generator=g)).to(torch.bfloat16)
+    for weight in (w, None):
+        q = torch.empty(600, 6144, dtype=F8, device="cuda")
+        sc = torch.empty(600, 48, device="cuda")
+        cm.coli_add_rmsnorm_fp8(x.cuda(), None, None if weight is None else weight.cuda(), 1e-6, None, None, q, sc)
+        y = x.double() * (1 if weight is None else weight.double())
+        v = 448 * y / ref.spread(y.abs().view(600, -1, 128).amax(-1), 6144, 1)
+        got = ref.decode(q)
+        lo, hi = ref.e4m3_round(v * (1 - 2.01 * U)), ref.e4m3_round(v * (1 + 2.01 * U))
+        assert ((got == lo) | (got == hi)).all()
+
+
+def test_norm_of_extreme_weights(cm):
+    """Weights whose product with the row leaves fp32's exact range: the codes then
+    come from n itself."""
+    x = torch.randn(3, 256, generator=torch.Generator().manual_seed(71)).to(torch.bfloat16)
+    for w in (1e37, 1e-30):
+        _norm_check(cm, x, None, torch.full((256,), w).to(torch.bfloat16))
