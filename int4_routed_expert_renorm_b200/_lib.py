@@ -8,6 +8,7 @@ library is missing the import fails loudly.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -173,6 +174,18 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _stream_scope(stream, device):
+    """The scope in which a holder makes the tensors that it hands to calls on
+    `stream` (None: the current one): memory that the allocator ties to that
+    stream, so that it is handed out again only behind the kernels that use it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                           device=device)
+    return torch.cuda.stream(stream)
 
 
 def _check(st: int, where: str):

@@ -2,7 +2,9 @@
 scale for each 128 x 128 block, and the layer's path over them.
 
 Argument marshalling only: ``Fp8MoELayer.forward`` is the library's norm, route,
-union and expert-FFN calls one after the other on one stream.
+union and expert-FFN calls one after the other on one stream.  The holder's
+methods make the arrays between those calls; they belong to the stream that the
+calls run on, and so do the tensors that are returned.
 """
 from __future__ import annotations
 
@@ -10,9 +12,9 @@ import ctypes
 
 import torch
 
-from ._lib import (COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, ColiError, coli_add_rmsnorm_fp8, coli_moe_dims,
-                   coli_moe_expert_ffn_fp8, coli_moe_fp8_workspace_bytes, coli_moe_route, coli_moe_union,
-                   coli_moe_weights_fp8)
+from ._lib import (COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, ColiError, _stream_scope, coli_add_rmsnorm_fp8,
+                   coli_moe_dims, coli_moe_expert_ffn_fp8, coli_moe_fp8_workspace_bytes, coli_moe_route,
+                   coli_moe_union, coli_moe_weights_fp8)
 
 _BLOCK = 128
 
@@ -60,30 +62,33 @@ class Fp8MoELayer:
     def norm(self, x, residual=None, sum_out=None, norm_out=None, stream=None):
         """(codes, scales) of the normalised rows of x (+ residual)."""
         T, H = x.shape
-        q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
-        s = torch.empty((T, H // _BLOCK), dtype=torch.float32, device=x.device)
-        coli_add_rmsnorm_fp8(x, residual, self.norm_weight, self.eps, sum_out, norm_out, q, s, stream)
+        with _stream_scope(stream, x.device):
+            q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=x.device)
+            s = torch.empty((T, H // _BLOCK), dtype=torch.float32, device=x.device)
+            coli_add_rmsnorm_fp8(x, residual, self.norm_weight, self.eps, sum_out, norm_out, q, s, stream)
         return q, s
 
     def experts(self, q, s, topk_ids, topk_w, out, ws, residual=None, stream=None):
         """Union, expert FFN and combine of a routed batch of codes ``q`` with scales ``s``."""
         T, E, P = q.shape[0], self.dims.n_experts, topk_ids.numel()
         new = lambda n: torch.empty(n, dtype=torch.int32, device=q.device)  # noqa: E731
-        unique, n_unique, seg, perm, pos = new(min(E, P)), new(1), new(min(E, P) + 1), new(P), new(P)
-        if T:
-            coli_moe_union(topk_ids, E, unique, n_unique, seg, perm, pos, stream)
-            coli_moe_expert_ffn_fp8(self.dims, self.weights, q, s, topk_ids, topk_w, unique, n_unique, seg, perm, pos,
-                                    residual, out, ws, stream)
+        with _stream_scope(stream, q.device):
+            unique, n_unique, seg, perm, pos = new(min(E, P)), new(1), new(min(E, P) + 1), new(P), new(P)
+            if T:
+                coli_moe_union(topk_ids, E, unique, n_unique, seg, perm, pos, stream)
+                coli_moe_expert_ffn_fp8(self.dims, self.weights, q, s, topk_ids, topk_w, unique, n_unique, seg, perm,
+                                        pos, residual, out, ws, stream)
         return out
 
     def forward(self, x, logits, out, ws, bias=None, residual=None, stream=None):
         """out = x' + experts(norm(x')), x' = x + residual, routed by ``logits``
         fp32 [T, E] (+ bias).  Returns (topk_ids, topk_w)."""
         T, k = x.shape[0], self.dims.top_k
-        h = x if residual is None else torch.empty_like(x)
-        q, s = self.norm(x, residual, None if residual is None else h, None, stream)
-        ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
-        w = torch.empty((T, k), dtype=torch.float32, device=x.device)
-        coli_moe_route(logits, bias, ids, w, stream)
-        self.experts(q, s, ids, w, out, ws, h, stream)
+        with _stream_scope(stream, x.device):
+            h = x if residual is None else torch.empty_like(x)
+            q, s = self.norm(x, residual, None if residual is None else h, None, stream)
+            ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+            w = torch.empty((T, k), dtype=torch.float32, device=x.device)
+            coli_moe_route(logits, bias, ids, w, stream)
+            self.experts(q, s, ids, w, out, ws, h, stream)
         return ids, w

@@ -1,0 +1,59 @@
+"""Holders called on another stream than the current one, which goes on allocating
+and writing blocks of the sizes that the holder's own arrays have."""
+import pytest
+import torch
+
+from tests import _fp8 as ref
+from tests._gpu import needs_gpu
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+
+
+@pytest.fixture(scope="module")
+def cm():
+    import int4_routed_expert_renorm_b200 as m
+    return m
+
+
+def _fp8_layer(cm, dims, seed):
+    g = torch.Generator().manual_seed(seed)
+    t = {}
+    n, H, I = dims.n_experts + dims.n_shared, dims.hidden, dims.inter
+    for name, R, K in (("gate", I, H), ("up", I, H), ("down", H, I)):
+        q, s = ref.block_quantise(torch.randn(n, R, K, generator=g, dtype=torch.float64) / K ** 0.5, 128)
+        t[name + "_q"], t[name + "_s"] = q.cuda(), s.cuda()
+    return cm.Fp8MoELayer(dims, t, (1 + 0.1 * torch.randn(H, generator=g)).to(torch.bfloat16).cuda())
+
+
+@pytest.mark.parametrize("T", [7, 90])           # gathered copies; pair order
+@pytest.mark.parametrize("handle", ["stream", "number", "default"])
+def test_fp8_layer_on_another_stream(cm, T, handle):
+    """The other stream is held up by 20 ms or so, so that its kernels run behind the
+    current stream's writes.  Every array of the call keeps its contents: the bits of
+    the call on the current stream."""
+    E, k, S, H, I = 12, 3, 1, 384, 256
+    layer = _fp8_layer(cm, cm.dims_for(H, I, E, k, S, group=128, code_bits=8), T)
+    g = torch.Generator().manual_seed(T + 1)
+    x, r = (torch.randn(T, H, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    logits = torch.randn(T, E, generator=g).cuda()
+    ws = layer.workspace(T)
+    want = torch.empty_like(x)
+    want_ids, want_w = layer.forward(x, logits, want, ws, residual=r)
+    want_q, want_s = layer.norm(x, r)
+    out = torch.zeros_like(x)
+    side = torch.cuda.default_stream() if handle == "default" else torch.cuda.Stream()
+    current = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(current):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)
+        arg = side if handle == "stream" else side.cuda_stream
+        ids, w = layer.forward(x, logits, out, ws, residual=r, stream=arg)
+        q, s = layer.norm(x, r, stream=arg)
+        sizes = [x.nbytes, T * H, T * H // 32, 4 * T * k, 4 * min(E, T * k), 4 * (min(E, T * k) + 1), 4]
+        spoil = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+        assert len(spoil) == 28
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(ids, want_ids) and torch.equal(w, want_w)
+    assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8)) and torch.equal(s, want_s)
+    assert cm.coli_moe_get_status() == (0, 0)
