@@ -10,9 +10,9 @@ import ctypes
 import numpy as np
 import torch
 
-from ._lib import (COLI_ERR_INVALID_ARG, ColiError, coli_moe_dims, coli_moe_layer_tiered, coli_moe_tier,
-                   coli_moe_tier_lookahead, coli_moe_tier_prefetch, coli_moe_tier_reset, coli_moe_tier_state_bytes,
-                   coli_moe_weights, coli_moe_workspace_bytes)
+from ._lib import (COLI_ERR_INVALID_ARG, ColiError, _stream_scope, coli_moe_dims, coli_moe_layer_tiered,
+                   coli_moe_tier, coli_moe_tier_lookahead, coli_moe_tier_prefetch, coli_moe_tier_reset,
+                   coli_moe_tier_state_bytes, coli_moe_weights, coli_moe_workspace_bytes)
 
 _NAMES = ("gate_q", "up_q", "down_q", "gate_s", "up_s", "down_s")
 
@@ -65,7 +65,8 @@ class TieredLayer:
 
     def prefetch(self, ids: torch.Tensor, stream=None):
         """Place experts `ids` (device int32, at most n_slots) ahead of use."""
-        coli_moe_tier_prefetch(self.dims, self.weights, self.tier, ids.contiguous(), stream)
+        with _stream_scope(stream, ids.device):        # a dense copy of strided ids is made on `stream`
+            coli_moe_tier_prefetch(self.dims, self.weights, self.tier, ids.contiguous(), stream)
 
     def lookahead(self, x: torch.Tensor, ws: torch.Tensor, flags: int = 0, stream=None):
         """Route x (the previous layer's input, on the device) with this
@@ -89,13 +90,14 @@ class TieredLayer:
         if u.size != E or (u < 0).any():
             raise ValueError(f"usage: {u.size} non-negative counts needed, one per expert ({E})")
         u = np.minimum(u, 0xFFFFFFFF).astype(np.uint32)
-        words = torch.from_numpy(u.view(np.int32).copy()).to(self.state.device)
+        words = torch.from_numpy(u.view(np.int32).copy())
         C = self.n_slots
         off = 4 * (E + C)                                   # usage[E] follows slot_of[E] and owner[C]
-        torch.cuda.synchronize()
-        self.state[off:off + 4 * E].copy_(words.view(torch.uint8))
         hot = np.lexsort((np.arange(E), -u.astype(np.int64)))[:C].astype(np.int32)
-        self.prefetch(torch.from_numpy(hot).to(self.state.device), stream)
+        torch.cuda.synchronize()
+        with _stream_scope(stream, self.state.device):      # the copies run ahead of the placement, on its stream
+            self.state[off:off + 4 * E].copy_(words.view(torch.uint8))
+            self.prefetch(torch.from_numpy(hot).to(self.state.device), stream)
 
     # ---- the state, read back (synchronises) ------------------------------
     def _words(self) -> np.ndarray:

@@ -57,3 +57,34 @@ def test_fp8_layer_on_another_stream(cm, T, handle):
     assert torch.equal(out, want) and torch.equal(ids, want_ids) and torch.equal(w, want_w)
     assert torch.equal(q.view(torch.uint8), want_q.view(torch.uint8)) and torch.equal(s, want_s)
     assert cm.coli_moe_get_status() == (0, 0)
+
+
+def test_tier_warm_start_on_another_stream(cm):
+    """The usage profile and the placement follow each other on the given stream, held
+    up here while the current stream writes blocks of their sizes."""
+    import numpy as np
+    import synth
+    import synth.gpu as sg
+    E, k, C = 32, 2, 6
+    shape = synth.LayerShape("tier_side", 512, 256, E, k, 1, 2)
+    dims = cm.dims_for(512, 256, E, k, 1)
+    tl = cm.TieredLayer(dims, sg.expert_tensors(shape), C)
+    profile = np.zeros(E, np.int64)
+    profile[[3, 9, 10, 21, 30, 31, 7]] = [50, 40, 40, 30, 20, 20, 20]
+    side = torch.cuda.Stream()
+    ids = torch.tensor([5, 0, 6, 0], dtype=torch.int32, device="cuda")[::2]
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        tl.reset()
+        tl.warm_from_usage(profile, stream)
+        spoil = [torch.full((n,), 1, dtype=torch.int32, device="cuda") for n in (C, E) for _ in range(4)]
+        st = tl.state_arrays()
+        assert sorted(st["owner"].tolist()) == [3, 7, 9, 10, 21, 30] and len(spoil) == 8
+        assert np.array_equal(st["usage"], profile.astype(np.uint32))
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)
+        tl.prefetch(ids, stream)                # strided: the holder makes a dense copy
+        spoil = [torch.full((2,), 1, dtype=torch.int32, device="cuda") for _ in range(4)]
+        owner = tl.state_arrays()["owner"].tolist()
+        assert 5 in owner and 6 in owner and 1 not in owner
+    assert cm.coli_moe_get_status() == (0, 0)

@@ -82,3 +82,26 @@ def test_fp8_layer(cm, monkeypatch, made, stream):
                 assert (on is None) if stream is None else (on is not None and on.cuda_stream == 0x70), (name, t.shape)
                 used += 1
     assert used >= 2 * (2 + 2 + 5 + 5)
+
+
+@pytest.mark.parametrize("stream", [None, FakeStream(0x70), 0x70])
+def test_tier_warm_start(cm, monkeypatch, made, stream):
+    """The profile's words, the hottest experts' ids and a dense copy of strided ids
+    are made and copied on the stream that places them."""
+    dims = cm.dims_for(256, 256, 8, 2, 0)
+    tl = object.__new__(cm.TieredLayer)
+    tl.dims, tl.n_slots, tl.weights, tl.tier = dims, 3, None, None
+    tl.state = torch.zeros(4 * (8 + 3 + 8 + 64), dtype=torch.uint8)
+    copies = []
+    copy = torch.Tensor.copy_
+    monkeypatch.setattr(torch.Tensor, "copy_", lambda a, b: (copies.append(torch.empty(1)), copy(a, b))[1])
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda: None)
+    seen = _calls(monkeypatch, cm.tier, ("coli_moe_tier_prefetch",))
+    tl.warm_from_usage(np.array([5, 0, 9, 1, 7, 0, 0, 2]), stream)
+    tl.prefetch(torch.arange(6, dtype=torch.int32)[::2], stream)
+    assert [a[3].tolist() for _, a in seen] == [[2, 4, 0], [0, 2, 4]] and len(copies) == 1
+    for t in copies + [a[3] for _, a in seen]:
+        on = made[t.data_ptr()]
+        assert (on is None) if stream is None else (on is not None and on.cuda_stream == 0x70)
+    assert all(a[-1] is stream for _, a in seen)
+    assert tl.state.view(torch.int32)[11:19].tolist() == [5, 0, 9, 1, 7, 0, 0, 2]
