@@ -8,11 +8,9 @@ calls run on, and so do the tensors that are returned.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
 
-from ._lib import (COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, ColiError, _stream_scope, coli_add_rmsnorm_fp8,
+from ._lib import (_E4M3, _F32, COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, ColiError, _stream_scope, coli_add_rmsnorm_fp8,
                    coli_moe_dims, coli_moe_expert_ffn_fp8, coli_moe_fp8_workspace_bytes, coli_moe_route,
                    coli_moe_union, coli_moe_weights_fp8)
 
@@ -22,17 +20,21 @@ _BLOCK = 128
 def fp8_weights(gate_q, up_q, down_q, gate_s, up_s, down_s) -> coli_moe_weights_fp8:
     """The C struct of an expert set: codes e4m3 (or their bytes) gate/up [E+S, I,
     H] and down [E+S, H, I], scales fp32 [E+S, I/128, H/128] and [E+S, H/128,
-    I/128].  The tensors stay the caller's: keep them alive while it is used."""
+    I/128], all on one device.  The tensors stay the caller's: keep them alive while
+    it is used."""
     n, I, H = gate_q.shape
     nh, ni = H // _BLOCK, I // _BLOCK
-    for name, t, shape, esize in (("gate_q", gate_q, (n, I, H), 1), ("up_q", up_q, (n, I, H), 1),
-                                  ("down_q", down_q, (n, H, I), 1), ("gate_s", gate_s, (n, ni, nh), 4),
-                                  ("up_s", up_s, (n, ni, nh), 4), ("down_s", down_s, (n, nh, ni), 4)):
-        if t.shape != shape or t.element_size() != esize:
-            raise ValueError(f"{name}: {tuple(t.shape)} of {t.dtype}, needs {shape} of {esize}-byte elements")
-    for t in (gate_q, up_q, down_q, gate_s, up_s, down_s):
+    named = (("gate_q", gate_q, (n, I, H), _E4M3), ("up_q", up_q, (n, I, H), _E4M3), ("down_q", down_q, (n, H, I), _E4M3),
+             ("gate_s", gate_s, (n, ni, nh), _F32), ("up_s", up_s, (n, ni, nh), _F32), ("down_s", down_s, (n, nh, ni), _F32))
+    for name, t, shape, types in named:
+        if t.shape != shape or t.dtype not in types:
+            names = " or ".join(str(x).replace("torch.", "") for x in types)
+            raise ValueError(f"{name}: {tuple(t.shape)} of {t.dtype}, needs {shape} of {names}")
+    for name, t, *_ in named:
         if not t.is_contiguous() or not t.is_cuda:
             raise ValueError("the experts' codes and scales must be dense tensors in device memory")
+        if t.get_device() != gate_q.get_device():
+            raise ValueError(f"{name}: a tensor on {t.device}, but gate_q is on {gate_q.device}")
     return coli_moe_weights_fp8(gate_q.data_ptr(), up_q.data_ptr(), down_q.data_ptr(), gate_s.data_ptr(),
                                 up_s.data_ptr(), down_s.data_ptr())
 
