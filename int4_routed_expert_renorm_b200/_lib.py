@@ -523,6 +523,10 @@ def coli_moe_expert_ffn_fp8(dims, weights, x, x_scale, topk_ids, topk_w, unique_
     T, H = _rows(x, "x")
     if H != dims.hidden:
         raise ValueError(f"x: shape {tuple(x.shape)}, the call needs [T, {dims.hidden}]")
+    made = getattr(weights, "made_of", None)        # None: a struct filled in by hand
+    if made is not None and made[:3] != (dims.n_experts + dims.n_shared, dims.inter, dims.hidden):
+        raise ValueError(f"weights: {made[0]} experts of {made[1]} x {made[2]}, the dims need "
+                         f"{dims.n_experts + dims.n_shared} of {dims.inter} x {dims.hidden}")
     P = T * dims.top_k
     U = min(dims.n_experts, P)
     p = _args(("x", x, _E4M3, None, False), ("x_scale", x_scale, _F32, T * (H // 128), False),
@@ -531,6 +535,8 @@ def coli_moe_expert_ffn_fp8(dims, weights, x, x_scale, topk_ids, topk_w, unique_
               ("seg_off", seg_off, _I32, U + 1, True), ("perm", perm, _I32, P, True),
               ("pair_pos", pair_pos, _I32, P, True), ("residual", residual, _BF16, T * H, False),
               ("out", out, _BF16, T * H, False), ("ws", ws, _ANY, None, False))
+    if made is not None and made[3] != p[-1]:
+        raise ValueError(f"weights: tensors on cuda:{made[3]}, but the call runs on cuda:{p[-1]}")
     st = _lib.coli_moe_expert_ffn_fp8(ctypes.byref(dims), ctypes.byref(weights), p[0], p[1], T, p[2], p[3], p[4], p[5],
                                       p[6], p[7], p[8], p[9], p[10], p[11], ws.nbytes, _raw_stream(stream, p[-1]))
     if st:

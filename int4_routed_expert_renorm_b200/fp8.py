@@ -35,8 +35,10 @@ def fp8_weights(gate_q, up_q, down_q, gate_s, up_s, down_s) -> coli_moe_weights_
             raise ValueError("the experts' codes and scales must be dense tensors in device memory")
         if t.get_device() != gate_q.get_device():
             raise ValueError(f"{name}: a tensor on {t.device}, but gate_q is on {gate_q.device}")
-    return coli_moe_weights_fp8(gate_q.data_ptr(), up_q.data_ptr(), down_q.data_ptr(), gate_s.data_ptr(),
-                                up_s.data_ptr(), down_s.data_ptr())
+    w = coli_moe_weights_fp8(gate_q.data_ptr(), up_q.data_ptr(), down_q.data_ptr(), gate_s.data_ptr(),
+                             up_s.data_ptr(), down_s.data_ptr())
+    w.made_of = (n, I, H, gate_q.get_device())      # compared with the dims and the device of each call
+    return w
 
 
 class Fp8MoELayer:

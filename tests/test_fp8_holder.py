@@ -71,3 +71,49 @@ def test_weights_refuse_scales_of_another_type(cm, name, dtype):
 def test_weights_refuse_tensors_of_two_devices(cm, name):
     with pytest.raises(ValueError, match=f"{name}.*cuda:1"):
         cm.fp8_weights(**_set(**{name: dict(gpu=1)}))
+
+
+def _call(cm, dims, weights, T=3):
+    H, P = dims.hidden, T * dims.top_k
+    U = min(dims.n_experts, P)
+    i32 = lambda *s: Dev(s, torch.int32)  # noqa: E731
+    ws = Dev((1 << 20,), torch.uint8)
+    ws.nbytes = 1 << 20
+    cm.coli_moe_expert_ffn_fp8(dims, weights, Dev((T, H), torch.uint8), Dev((T, H // 128), torch.float32),
+                               i32(T, dims.top_k), Dev((T, dims.top_k), torch.float32), i32(U), i32(1), i32(U + 1), i32(P),
+                               i32(P), None, Dev((T, H), torch.bfloat16), ws, 0)
+
+
+@pytest.fixture
+def no_launch(cm, monkeypatch):
+    """The C entry counts its calls instead; the current device is GPU 0."""
+    class Lib:
+        calls = 0
+
+        def coli_moe_expert_ffn_fp8(self, *a):
+            Lib.calls += 1
+            return 0
+
+    monkeypatch.setattr(cm._lib, "_lib", Lib())
+    monkeypatch.setattr(cm._lib, "_current_device", lambda: 0)
+    return Lib
+
+
+@pytest.mark.parametrize("E,S,I,H", [(5, 1, 128, 256), (3, 1, 128, 256), (4, 1, 256, 256), (4, 1, 128, 384), (4, 2, 128, 256)])
+def test_call_refuses_weights_of_other_dims(cm, no_launch, E, S, I, H):
+    """More experts or longer rows than the set has would be read past its end."""
+    with pytest.raises(ValueError, match="weights: 5 experts of 128 x 256"):
+        _call(cm, cm.dims_for(H, I, E, 2, S, group=128, code_bits=8), cm.fp8_weights(**_set()))
+    assert no_launch.calls == 0
+
+
+def test_call_refuses_weights_on_another_device(cm, no_launch):
+    t = {n: Dev(s, torch.uint8 if n[-1] == "q" else torch.float32, gpu=1) for n, s in SHAPES.items()}
+    dims = cm.dims_for(256, 128, 4, 2, 1, group=128, code_bits=8)
+    with pytest.raises(ValueError, match="weights: tensors on cuda:1, but the call runs on cuda:0"):
+        _call(cm, dims, cm.fp8_weights(**t))
+    assert no_launch.calls == 0
+    _call(cm, dims, cm.fp8_weights(**_set()))
+    _call(cm, cm.dims_for(256, 128, 5, 2, 0, group=128, code_bits=8), cm.fp8_weights(**_set()))   # the same 5 experts
+    _call(cm, dims, cm.coli_moe_weights_fp8(*[0x10000] * 6))       # by hand: the caller answers for it
+    assert no_launch.calls == 3
