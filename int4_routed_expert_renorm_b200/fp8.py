@@ -10,9 +10,9 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import (_E4M3, _F32, COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, ColiError, _stream_scope, coli_add_rmsnorm_fp8,
-                   coli_moe_dims, coli_moe_expert_ffn_fp8, coli_moe_fp8_workspace_bytes, coli_moe_route,
-                   coli_moe_union, coli_moe_weights_fp8)
+from ._lib import (_BF16, _E4M3, _F32, COLI_ERR_INVALID_ARG, COLI_ERR_UNSUPPORTED, ColiError, _stream_scope,
+                   coli_add_rmsnorm_fp8, coli_moe_dims, coli_moe_expert_ffn_fp8, coli_moe_fp8_workspace_bytes,
+                   coli_moe_route, coli_moe_union, coli_moe_weights_fp8)
 
 _BLOCK = 128
 
@@ -54,6 +54,12 @@ class Fp8MoELayer:
         if tuple(self.t["gate_q"].shape) != want:
             raise ValueError(f"gate_q: {tuple(self.t['gate_q'].shape)}, the dims need {want}")
         self.weights = fp8_weights(**{m: self.t[m] for m in ("gate_q", "up_q", "down_q", "gate_s", "up_s", "down_s")})
+        if norm_weight is not None:
+            if norm_weight.numel() != dims.hidden or norm_weight.dtype not in _BF16:
+                raise ValueError(f"norm_weight: {norm_weight.numel()} elements of {norm_weight.dtype}, the dims need "
+                                 f"{dims.hidden} of bfloat16")
+            if not norm_weight.is_contiguous() or norm_weight.get_device() != self.weights.made_of[3]:
+                raise ValueError(f"norm_weight: needs a dense tensor on cuda:{self.weights.made_of[3]}")
         self.norm_weight, self.eps = norm_weight, eps
 
     def workspace(self, t_max: int, device="cuda") -> torch.Tensor:

@@ -117,3 +117,15 @@ def test_call_refuses_weights_on_another_device(cm, no_launch):
     _call(cm, cm.dims_for(256, 128, 5, 2, 0, group=128, code_bits=8), cm.fp8_weights(**_set()))   # the same 5 experts
     _call(cm, dims, cm.coli_moe_weights_fp8(*[0x10000] * 6))       # by hand: the caller answers for it
     assert no_launch.calls == 3
+
+
+def test_layer_checks_its_norm_weight_when_it_is_built(cm):
+    dims = cm.dims_for(256, 128, 4, 2, 1, group=128, code_bits=8)
+    strided = Dev((256,), torch.bfloat16)
+    strided.is_contiguous = lambda: False
+    for bad in (Dev((128,), torch.bfloat16), Dev((256,), torch.float32), Dev((256,), torch.float16),
+                Dev((256,), torch.bfloat16, gpu=1), torch.ones(256, dtype=torch.bfloat16), strided):
+        with pytest.raises(ValueError, match="norm_weight"):
+            cm.Fp8MoELayer(dims, _set(), bad)
+    for good in (None, Dev((256,), torch.bfloat16), Dev((256,), torch.int16)):
+        assert cm.Fp8MoELayer(dims, _set(), good).norm_weight is good
