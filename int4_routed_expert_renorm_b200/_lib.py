@@ -382,8 +382,10 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8, torch.int8)
 _ANY = None
 
 
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The quick forms of torch.cuda.current_device and current_stream, where this torch has them.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                   or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
 def _refuse(specs):

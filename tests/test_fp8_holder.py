@@ -129,3 +129,25 @@ def test_layer_checks_its_norm_weight_when_it_is_built(cm):
             cm.Fp8MoELayer(dims, _set(), bad)
     for good in (None, Dev((256,), torch.bfloat16), Dev((256,), torch.int16)):
         assert cm.Fp8MoELayer(dims, _set(), good).norm_weight is good
+
+
+def test_binding_without_the_quick_device_and_stream_lookups(cm, monkeypatch):
+    """On a torch without them the public forms answer: the call reaches the library
+    with the current stream's handle."""
+    import importlib.util
+    from types import SimpleNamespace
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: SimpleNamespace(cuda_stream=0x70 + device))
+    spec = importlib.util.spec_from_file_location("int4_routed_expert_renorm_b200._lib_other", cm._lib.__file__)
+    other = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(other)
+    seen = []
+    other._lib = SimpleNamespace(coli_fp8_matmul=lambda *a: seen.append(a) or 0)
+    a, w = Dev((3, 256), torch.uint8), Dev((128, 256), torch.uint8)
+    other.coli_fp8_matmul(a, Dev((3, 2), torch.float32), w, Dev((1, 2), torch.float32), Dev((3, 128), torch.float32))
+    assert len(seen) == 1 and seen[0][-1] == 0x70
+    with pytest.raises(ValueError, match="current device is cuda:0"):
+        other.coli_fp8_matmul(Dev((3, 256), torch.uint8, gpu=1), Dev((3, 2), torch.float32), w, Dev((1, 2), torch.float32),
+                              Dev((3, 128), torch.float32))
