@@ -91,7 +91,8 @@ std::mutex g_mu;
 uint32_t* g_status_ptr[kMaxDevices] = {};
 int g_num_sms[kMaxDevices] = {};
 bool g_attr_done[kMaxDevices] = {};
-bool g_fp8_ok[kMaxDevices] = {};
+bool g_balance_ready[kMaxDevices] = {};
+bool g_fp8_ready[kMaxDevices] = {};
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 // Shared memory of the 8-bit product's kernels.  Their setmaxnreg split hands out
@@ -132,7 +133,7 @@ bool balance_kernels_ready() {
 struct DevInfo {
   uint32_t* status;
   int sms;
-  bool fp8;   // the 8-bit product's kernels may run
+  int dev;
 };
 
 coli_status dev_info(DevInfo* out) {
@@ -183,8 +184,6 @@ coli_status dev_info(DevInfo* out) {
     COLI_SET_SK_SMEM(1, 64, 8)
     COLI_SET_SK_SMEM(2, 64, 8)
 #undef COLI_SET_SK_SMEM
-    ok &= balance_kernels_ready();
-    g_fp8_ok[dev] = fp8_kernels_ready();
     ok &= cudaFuncSetAttribute(logits_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
           cudaSuccess;
     ok &= cudaFuncSetAttribute(union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -211,8 +210,16 @@ coli_status dev_info(DevInfo* out) {
   }
   out->status = g_status_ptr[dev];
   out->sms = g_num_sms[dev];
-  out->fp8 = g_fp8_ok[dev];
+  out->dev = dev;
   return COLI_OK;
+}
+
+// Whether kernels that other calls do not use may run on device `dev`: `prepare`
+// is asked at the first call that needs them, so that no other call loads them or
+// fails for them, and again after a failure.
+bool kernels_ready(int dev, bool* ready, bool (*prepare)()) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  return ready[dev] || (ready[dev] = prepare());
 }
 
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }

@@ -178,7 +178,7 @@ coli_status coli_moe_balance(const float* logits, const float* bias, const int32
   const BalWs w = balance_layout(std::max(T, 1), E, ws);
   if (ws_bytes < w.bytes) return COLI_ERR_WORKSPACE;
   DevInfo di;
-  if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
+  if (dev_info(&di) != COLI_OK || !kernels_ready(di.dev, g_balance_ready, balance_kernels_ready)) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
   const int blocks = balance_blocks(T);
   const bool fused = balance_fused(T);
@@ -210,7 +210,7 @@ coli_status coli_moe_balance_backward(const float* logits, const float* bias, co
   const BalWs w = balance_layout(std::max(T, 1), E, ws);
   if (ws_bytes < w.bytes) return COLI_ERR_WORKSPACE;
   DevInfo di;
-  if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
+  if (dev_info(&di) != COLI_OK || !kernels_ready(di.dev, g_balance_ready, balance_kernels_ready)) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
   const int blocks = balance_blocks(T);
   const bool fused = balance_fused(T);
@@ -268,7 +268,7 @@ coli_status coli_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4))
     return COLI_ERR_INVALID_ARG;
   DevInfo di;
-  if (dev_info(&di) != COLI_OK || !di.fp8) return COLI_ERR_CUDA;
+  if (dev_info(&di) != COLI_OK || !kernels_ready(di.dev, g_fp8_ready, fp8_kernels_ready)) return COLI_ERR_CUDA;
   const int nk = (K + kF8Block - 1) / kF8Block, nrb = (N + kF8Block - 1) / kF8Block;
   F8Args g{};
   g.a_s = a_scale;
@@ -325,7 +325,7 @@ coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims* dims, const coli_moe_we
   const F8Ws lay = fp8_layout(dims, T, ws);
   if (ws_bytes < lay.bytes) return COLI_ERR_WORKSPACE;
   DevInfo di;
-  if (dev_info(&di) != COLI_OK || !di.fp8) return COLI_ERR_CUDA;
+  if (dev_info(&di) != COLI_OK || !kernels_ready(di.dev, g_fp8_ready, fp8_kernels_ready)) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
   const int H = dims->hidden, I = dims->inter, E = dims->n_experts, k = dims->top_k, S = dims->n_shared, P = T * k;
   F8Args g{};
