@@ -91,7 +91,7 @@ typedef enum {
 
 /* Device status bits (coli_moe_get_status). */
 #define COLI_FLAG_NONFINITE 0x1u  /* a logit was NaN or +inf, or a selected logit was -inf; or a row of
-                                   * coli_add_rmsnorm_fp8 has no finite sum of squares */
+                                   * coli_add_rmsnorm_fp8 holds NaN or an infinity */
 #define COLI_FLAG_BAD_ID    0x2u  /* an expert id outside [0, E) reached the union or coli_moe_balance */
 #define COLI_FLAG_TIMEOUT   0x4u  /* a bounded pipeline wait expired; outputs are undefined */
 #define COLI_FLAG_RANGE     0x8u  /* the prefill form met an expert input or h value of magnitude
@@ -481,8 +481,11 @@ size_t coli_moe_balance_workspace_bytes(int T_max, int E);
  *   norm_out bf16 [T][H] or NULL: bf16(n), e.g. the router's input
  *   q        e4m3 [T][H] (bytes), q_scale fp32 [T][H/128]: n ~ q * q_scale
  * H a multiple of 128, H <= 32768; bf16 tensors and q 16-byte aligned; eps >= 0.
- * A row whose sum of squares is not finite sets COLI_FLAG_NONFINITE; its
- * outputs are what the formulas give (NaN codes are 0x7f).
+ * Rows of any finite magnitude: where the mean of squares leaves fp32's normal
+ * numbers the row is taken in 64 bits.  n of a row of zeros is 0, with eps = 0
+ * too.  A row of s with NaN or an infinity sets COLI_FLAG_NONFINITE: NaN makes
+ * all its outputs NaN (codes 0x7f), an infinity those of its block and zeros of
+ * the others.
  */
 coli_status coli_add_rmsnorm_fp8(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps, int T,
                                  int H, uint16_t *sum_out, uint16_t *norm_out, uint8_t *q, float *q_scale,

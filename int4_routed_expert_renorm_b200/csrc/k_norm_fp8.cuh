@@ -54,13 +54,90 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   return float_to_bf16_bits(a) | (static_cast<uint32_t>(float_to_bf16_bits(b)) << 16);
 }
 
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const uint16_t* weight;
+  float eps;
+  int H;
+  uint16_t* sum_out;
+  uint16_t* norm_out;
+  uint8_t* q;
+  float* q_scale;
+  uint32_t* status;
+};
+
+// The rest of a block's row whose mean of squares plus eps is no normal fp32 number
+// (values past 1e19 whose squares overflow, values below 1e-19 with next to no eps, a
+// row of zeros with eps = 0, infinities, NaN): sum, root and n in 64 bits, where the
+// squares of bf16 numbers neither overflow nor vanish.  n of a row of zeros is 0
+// whatever eps.
+__device__ __forceinline__ void norm_row_wide(const NormArgs& a) {
+  __shared__ double wide_sm[8];
+  const int tid = threadIdx.x;
+  const size_t row = static_cast<size_t>(blockIdx.x) * a.H;
+  auto value = [&](int c) -> double {
+    if (a.sum_out) return bf16_bits_to_float(a.sum_out[row + c]);      // this thread wrote it
+    const float v = bf16_bits_to_float(a.x[row + c]);
+    return a.residual ? bf16_bits_to_float(float_to_bf16_bits(v + bf16_bits_to_float(a.residual[row + c]))) : v;
+  };
+  double ss = 0.0;
+#pragma unroll 1
+  for (int c = tid * 8; c < a.H; c += 2048)
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const double v = value(c + k);
+      ss += v * v;
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if ((tid & 31) == 0) wide_sm[tid >> 5] = ss;
+  __syncthreads();
+  ss = 0.0;
+#pragma unroll 1
+  for (int w = 0; w < 8; ++w) ss += wide_sm[w];
+  if (tid == 0 && !(ss < INFINITY)) atomicOr(a.status, COLI_FLAG_NONFINITE);
+  const double ms = ss / a.H + static_cast<double>(a.eps);
+  const double rs = ms == 0.0 ? 0.0 : 1.0 / sqrt(ms);
+  auto n_at = [&](int c) {
+    return static_cast<float>(value(c) * rs * (a.weight ? static_cast<double>(bf16_bits_to_float(a.weight[c])) : 1.0));
+  };
+  // as many rounds for every thread: a block's maximum is over 16 lanes
+#pragma unroll 1
+  for (int c0 = 0; c0 < a.H; c0 += 2048) {
+    const int c = c0 + tid * 8;
+    float m = 0.f;
+    if (c < a.H)
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(n_at(c + k)));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (c >= a.H) continue;
+    float inv;
+    const float sc = f8_scale(m, &inv);
+    if ((tid & 15) == 0) a.q_scale[(row + c) / kF8Block] = sc;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const float z = n_at(c + k);
+      a.q[row + c + k] = static_cast<uint8_t>(f8x4(z * inv, 0.f, 0.f, 0.f));
+      if (a.norm_out) a.norm_out[row + c + k] = float_to_bf16_bits(z);
+    }
+  }
+}
+
 // NC: 2048-column steps of a row (H <= 2048 * NC).  x, residual and sum_out may
 // be the same buffer: a thread reads its values before it writes them.
 template <int NC>
-__global__ void __launch_bounds__(256, NC <= 3 ? 5 : 1)
-    add_rmsnorm_fp8_kernel(const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ weight, float eps,
-                           int H, uint16_t* sum_out, uint16_t* __restrict__ norm_out, uint8_t* __restrict__ q,
-                           float* __restrict__ q_scale, uint32_t* __restrict__ status) {
+__global__ void __launch_bounds__(256, NC <= 1 ? 8 : NC <= 3 ? 5 : 1)
+    add_rmsnorm_fp8_kernel(const __grid_constant__ NormArgs a) {
+  const uint16_t* x = a.x;
+  const uint16_t* residual = a.residual;
+  const uint16_t* weight = a.weight;
+  uint16_t* sum_out = a.sum_out;
+  uint16_t* norm_out = a.norm_out;
+  uint8_t* q = a.q;
+  float* q_scale = a.q_scale;
+  const int H = a.H;
   __shared__ float sm[8];
   pdl_wait();
   pdl_trigger();
@@ -105,8 +182,11 @@ __global__ void __launch_bounds__(256, NC <= 3 ? 5 : 1)
   if (lane == 0) sm[warp] = ss;
   __syncthreads();
   ss = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
-  if (tid == 0 && !(ss < INFINITY)) atomicOr(status, COLI_FLAG_NONFINITE);
-  const float rs = 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
+  const float rs = 1.0f / sqrtf(ss / static_cast<float>(H) + a.eps);
+  // rs of a mean that is no normal number is 0, NaN or more than 2^63.  (Squares below
+  // fp32's normal numbers lose bits: 2^-150 of the mean at most, half a step of any
+  // normal one.)
+  const bool normal = rs > 0.f && rs <= 9.223372e18f;
   const int nb = H / kF8Block;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
@@ -127,8 +207,15 @@ __global__ void __launch_bounds__(256, NC <= 3 ? 5 : 1)
     for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     float rn = rs, mn = m * rs;      // n = y * rn, max|n|
     // s g at fp32's ends, where it is no longer exact (zeros and NaN among them): y becomes n
-    const bool exact = m > 1e-25f && m < 1e35f;
+    const bool exact = m > 1e-25f && m < 1e35f && normal;
     if (__any_sync(0xffffffffu, !exact)) {
+      // every warp of such a row's block comes here; asked here and not on the path of
+      // all other rows (65536 x 1024 142 us, 148 us with the call in front of this loop,
+      // 139 without it)
+      if (!normal) {
+        norm_row_wide(a);
+        return;
+      }
       float z[8];
       float mz = 0.f;
 #pragma unroll

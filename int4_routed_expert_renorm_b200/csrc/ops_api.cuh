@@ -245,10 +245,10 @@ coli_status coli_add_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, co
   if (dev_info(&di) != COLI_OK) return COLI_ERR_CUDA;
   const cudaStream_t s = as_stream(stream);
   const int nc = (H + 2047) / 2048;
+  const NormArgs a{x, residual, weight, eps, H, sum_out, norm_out, q, q_scale, di.status};
   bool ok;
-#define COLI_NORM(NC)                                                                                             \
-  launch(add_rmsnorm_fp8_kernel<NC>, dim3(T), dim3(256), 0, s, x, residual, weight, eps, H, sum_out, norm_out, q, \
-         q_scale, di.status)
+#define COLI_NORM(NC) \
+  launch(add_rmsnorm_fp8_kernel<NC>, dim3(T), dim3(256), 0, s, a)
   if (nc <= 1) ok = COLI_NORM(1);
   else if (nc <= 2) ok = COLI_NORM(2);
   else if (nc <= 3) ok = COLI_NORM(3);
