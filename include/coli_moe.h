@@ -501,7 +501,10 @@ coli_status coli_add_rmsnorm_fp8(const uint16_t *x, const uint16_t *residual, co
  * K a multiple of 16 (the last block may be short), K <= 2^20; any N <= 2^21, M
  * <= 2^24; M == 0 is a no-op.  a, w and out 16-byte aligned; out overlaps no
  * input.  A block's products are summed in fp32 on the tensor cores; the scaled
- * block sums are added in fp32 in a fixed order.
+ * block sums are added in fp32 in a fixed order: the same call gives the same
+ * bits.  The order depends on M, N and K (K is split over CTAs where tiles are
+ * few), so a row's last bits may differ between batches of other sizes.  The two
+ * scales are multiplied first, in fp32.
  */
 #define COLI_FP8_OUT_F32 0x1u
 coli_status coli_fp8_matmul(const uint8_t *a, const float *a_scale, const uint8_t *w, const float *w_scale, int M,
