@@ -30,10 +30,13 @@
 // their scale: g and u never leave the SM.
 // A operand rows past the tile's tokens are whatever shared memory holds; they
 // only reach tensor-memory lanes that nothing reads.
-// Measured on one B200: 8192 x 12288 x 6144 in 748 us (1.65 PFLOP/s; a K block of a
-// tile takes 1130 cycles, its MMAs 512, its copies alone 1035); 1 x 4096 x 6144 in
-// 11 us; the FFN of a 256-expert layer (H 6144, I 2048, top-8, one shared) in 76 us
-// for 1 token, 1.60 ms for 256 (HBM floor 1.48), 2.93 ms for 4096.
+// Measured on one B200, over calls as a program makes them (runs of seconds, where the
+// clock settles under the power cap; in brackets tens of passes): 8192 x 12288 x 6144
+// in 886 us (748), 1.40 PFLOP/s; 1 x 4096 x 6144 in 11 us; the FFN of a 256-expert layer
+// (H 6144, I 2048, top-8, one shared) in 85 us (76) for 1 token, 466 us for 64 tokens
+// over about 62 experts (HBM floor 357), 3.44 ms (2.93) for 4096.  A K block of a dense
+// tile takes about 1190 cycles, its MMAs 512, its copies alone 1035; the totals wait for
+// tensor memory most of the time (FMA pipe 30 % active, issue 0.41 per cycle).
 #pragma once
 #include <type_traits>
 
@@ -758,7 +761,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       if constexpr (GU) {
         if (!any) continue;
         // h, the maximum of the token's 128 columns (64 in each of two threads),
-        // codes and scale
+        // codes and scale.  A code sees two roundings before its own, of 1 / c and of
+        // the product (a division by c would be one, for 64 values a thread): half a
+        // step 2^-24 each, less than the sums of g and u are off by.
         float mx = 0.f, h[2][32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {

@@ -16,8 +16,9 @@
 // columns (one 16-byte load), so a 128-column block is 16 neighbouring lanes and
 // its maximum a 4-step shuffle.  The row is read once and stays in registers.
 // Bound by HBM for large batches (9.03 bytes per value with everything written)
-// and by latency for single tokens.  16384 x 6144 with residual, weight and all
-// outputs: 141 us, 6.45 TB/s (five blocks per SM; 146 us with four).
+// and by latency for single tokens (1 x 6144: 3.6 us).  16384 x 6144 with residual,
+// weight and all outputs: 137 us on one set of buffers, 6.6 TB/s, 146 us with others
+// from pass to pass (five blocks per SM; with four 3.5 % more).
 #pragma once
 #include <cuda_fp8.h>
 

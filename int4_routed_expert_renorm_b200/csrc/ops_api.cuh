@@ -285,6 +285,15 @@ coli_status coli_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
   const cudaStream_t s = as_stream(stream);
   const bool few = M <= kF8Few;
   const int64_t blocks = few ? 1 : (M + kF8Tokens - 1) / kF8Tokens;
+  // Two weight blocks a tile where such tiles fill the SMs: 48 KB of copies per K block
+  // for twice the products of 32 KB (2048 x 4608 x 6144, 288 tiles of two: 74 us, 84 with
+  // single blocks; 32 x 20480 x 6144, where the rule takes single ones in two waves, 41
+  // with two and 57 so).  Below, single blocks, and several CTAs per tile where those
+  // are fewer than the SMs too (1024 x 2048 x 6144, 128 tiles: 27 us, 39 with two).
+  // Between the two, where single-block tiles need a second wave and two-block ones do
+  // not, single blocks are 5 to 14 % slower (1024 x 4096 x 6144: 47 against 42 us); just
+  // above one wave of two-block tiles they would be 10 % faster (1024 x 5120 x 6144: 64
+  // against 72).
   const int64_t tiles1 = blocks * nrb, tiles2 = blocks * ((nrb + 1) / 2);
   bool ok;
   if (tiles2 >= di.sms) {
@@ -338,6 +347,13 @@ coli_status coli_moe_expert_ffn_fp8(const coli_moe_dims* dims, const coli_moe_we
   g.E = E;
   g.S = S;
   g.P = P;
+  // Tiles of 32 tokens with gathered copies, or of 128 in pair order behind a gather
+  // launch.  The short ones save that launch: one token of a layer of 64 experts (H 2048,
+  // I 1024) 43 against 48 us, of 256 experts (H 6144, I 2048) 92 against 95, cold.  They
+  // lose where more pairs come together: 64 tokens of the wide layer over 55 experts 532
+  // against 461 us, 512 over 118 1882 against 989.  Between 4 and 32 tokens it depends on
+  // the widths: 32 tokens 100 against 99 us in the small layer, 1183 against 1027 in the
+  // wide one, where the long tiles would be 3 to 13 % faster.
   const bool few = T <= kF8Few;
   const int nt = few ? kF8Few : kF8Tokens;
   const int64_t blocks_ub = static_cast<int64_t>(std::min(P, E)) + P / nt + static_cast<int64_t>(S) * (T / nt + 1);

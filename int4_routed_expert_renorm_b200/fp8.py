@@ -92,7 +92,11 @@ class Fp8MoELayer:
 
     def forward(self, x, logits, out, ws, bias=None, residual=None, stream=None):
         """out = x' + experts(norm(x')), x' = x + residual, routed by ``logits``
-        fp32 [T, E] (+ bias).  Returns (topk_ids, topk_w)."""
+        fp32 [T, E] (+ bias).  Returns (topk_ids, topk_w).
+
+        A router that reads the normalised row goes call by call, with one norm:
+        ``q, s = norm(x, residual, h, n)``, the logits from n, ``coli_moe_route``,
+        ``experts(q, s, ids, w, out, ws, h)``."""
         T, k = x.shape[0], self.dims.top_k
         with _stream_scope(stream, x.device):
             h = x if residual is None else torch.empty_like(x)
