@@ -88,3 +88,42 @@ def test_tier_warm_start_on_another_stream(cm):
         owner = tl.state_arrays()["owner"].tolist()
         assert 5 in owner and 6 in owner and 1 not in owner
     assert cm.coli_moe_get_status() == (0, 0)
+
+
+@pytest.mark.parametrize("fork", [False, True])
+def test_fp8_layer_in_a_graph(cm, fork):
+    """forward captured, on the capturing stream or on one that forks from it and joins
+    again, and replayed with other inputs while eager calls run in between."""
+    T, E, k, S, H, I = 40, 12, 3, 1, 384, 256
+    layer = _fp8_layer(cm, cm.dims_for(H, I, E, k, S, group=128, code_bits=8), 5)
+    g = torch.Generator().manual_seed(6)
+    ins = [[torch.randn(T, H, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+           + [torch.randn(T, E, generator=g).cuda()] for _ in range(3)]
+    ws, ws2 = layer.workspace(T), layer.workspace(T)
+
+    def eager(x, r, logits):
+        out = torch.empty_like(x)
+        ids, w = layer.forward(x, logits, out, ws, residual=r)
+        return out, ids, w
+
+    want = [eager(*i) for i in ins]
+    x, r, logits = (t.clone() for t in ins[0])
+    out, side = torch.zeros_like(x), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if fork:
+            side.wait_stream(torch.cuda.current_stream())
+            ids, w = layer.forward(x, logits, out, ws2, residual=r, stream=side)
+            torch.cuda.current_stream().wait_stream(side)
+        else:
+            ids, w = layer.forward(x, logits, out, ws2, residual=r)
+    for i, (o, oi, ow) in zip(ins, want):
+        for dst, src in zip((x, r, logits), i):
+            dst.copy_(src)
+        graph.replay()
+        again = eager(*i)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(ids, oi) and torch.equal(w, ow)
+        assert torch.equal(again[0], o)
+    assert cm.coli_moe_get_status() == (0, 0)
